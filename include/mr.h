@@ -603,6 +603,126 @@ int mr_combine(const void *expert_out, int dtype, const float *w,
                int d, int k, mr_stream_t stream);
 
 /*
+ * mr_combine_backward -- gradients of mr_combine (the same page; the forward's
+ * two roundings pass a gradient through unchanged, so the shared row's
+ * gradient is dy itself).
+ *
+ *   dy         [T, d] gradient of y, `dtype` MR_BF16 or MR_F32.
+ *   expert_out [T*k, d] the forward's expert outputs (read for dw only; may be
+ *              NULL when dw is).
+ *   w, inv_perm  as mr_combine.
+ *   dexpert    [T*k, d] of `dtype`, or NULL: row inv_perm[t*k+j] gets
+ *              w[t,j] * dy[t], rounded once.  Rows that no slot names (those
+ *              of dropped slots) are not written.
+ *   dw         [T, k] fp32, or NULL: dw[t,j] = sum_c dy[t,c] *
+ *              expert_out[inv_perm[t*k+j]][c] in fp32; 0 for a dropped slot.
+ * One kernel, no atomics: the results do not change from run to run.
+ * dexpert must not overlap dy or expert_out.  Limits: 1 <= k <= 32; at least
+ * one of dexpert and dw.
+ */
+int mr_combine_backward(const void *dy, int dtype, const void *expert_out,
+                        const float *w, const int32_t *inv_perm, int T, int d,
+                        int k, void *dexpert, float *dw, mr_stream_t stream);
+
+/*
+ * mr_gather_rows_backward -- gradient of mr_gather_rows: each token sums the
+ * gradients of its k sorted rows.
+ *
+ *   dxs       [T*k, d] gradients of the sorted rows, `dtype` MR_BF16 or MR_F32.
+ *   inv_perm  [T*k] from mr_dispatch; a slot whose entry is -1 adds nothing.
+ *   add       [T, d] of `dtype` added to the sum (the gradient of x's other
+ *             uses, e.g. the shared expert), or NULL.  May be dx itself.
+ *   dx        [T, d] of `dtype`: dx[t] = sum_j dxs[inv_perm[t*k+j]] + add[t],
+ *             summed in fp32 in slot order, rounded once.
+ * One kernel, no atomics.  Limits: 1 <= k <= 32.
+ */
+int mr_gather_rows_backward(const void *dxs, int dtype,
+                            const int32_t *inv_perm, const void *add, int T,
+                            int d, int k, void *dx, mr_stream_t stream);
+
+/*
+ * mr_router_backward -- gradient of the gate (mr_router_forward and its
+ * variants): from the router weights' gradient dw to the hidden states and the
+ * gate weight.  The choice of experts is piecewise constant and the bias only
+ * enters the choice, so neither has a gradient.  Per token, with s the scores
+ * and S the sum of the k chosen ones:
+ *   sigmoid  dL_e = route_scale / (S + 1e-20) * (dw_j - sum_i dw_i s_i / (S +
+ *            1e-20)) * s_e (1 - s_e) for the chosen e = idx[t,j], 0 elsewhere
+ *            (MR_NORM_NO_EPS: without the 1e-20);
+ *   softmax  dL_e = route_scale * s_e * ([e chosen] dw_j - sum_i dw_i s_i) for
+ *            every expert (MR_SCORE_SOFTMAX).
+ *   dx = dL . W + add,  dW = dL^T . x.
+ *
+ *   x         [T, d] of x_dtype (read for dW only).
+ *   W         [N_r, d] of W_dtype: MR_F32, or MR_BF16 for the gate of
+ *             mr_router_forward_bf16w (read for dx only).
+ *   logits    [T, N_r] fp32, the forward's logits_out.
+ *   idx       [T, k] int32, the forward's choice.  A slot whose id lies outside
+ *             [0, N_r) has no gradient and raises the device flag
+ *             (MR_ERR_DEVICE).
+ *   dw        [T, k] fp32, e.g. from mr_combine_backward.
+ *   perm, offsets   mr_dispatch of idx (read for dW with sigmoid scores only;
+ *             NULL allowed otherwise).
+ *   flags     those of the forward; MR_GROUP_MAX only concerns the choice.
+ *   add       [T, d] of x_dtype added to dx (the gradient of x's other uses,
+ *             e.g. from mr_gather_rows_backward), or NULL.  May be dx itself.
+ *   dlogits   [T, N_r] fp32 out, or NULL.
+ *   dx        [T, d] of x_dtype out, or NULL; rounded once.
+ *   dW        [N_r, d] fp32 out, or NULL; 0 for experts that no token chose
+ *             (sigmoid) and for T == 0.
+ *   workspace at least mr_router_backward_workspace_size(T, d, N_r, k, flags)
+ *             bytes, 16-byte aligned; its contents need no initialisation.
+ * All products and sums in fp32 (fp32-level accuracy), in a fixed order.
+ * Calls that may overlap need different workspaces.
+ * Limits: N_r <= 512, 1 <= k <= 32; at least one of dlogits, dx and dW.
+ */
+size_t mr_router_backward_workspace_size(int T, int d, int N_r, int k,
+                                         int flags);
+int mr_router_backward(const void *x, int x_dtype, const void *W, int W_dtype,
+                       const float *logits, const int32_t *idx,
+                       const float *dw, const int32_t *perm,
+                       const int32_t *offsets, int T, int d, int N_r, int k,
+                       float route_scale, int flags, const void *add,
+                       float *dlogits, void *dx, float *dW, void *workspace,
+                       size_t workspace_bytes, mr_stream_t stream);
+
+/*
+ * mr_expert_pack_w4 / mr_expert_gemv_gather_w4 -- the expert layer of
+ * mr_expert_gemm_gather on 4-bit weights with group scales, for batches of few
+ * tokens (decode), whose time is that of reading the weights:
+ *     out[j][n] = sum_G scales[e][n][G] * sum_{c in group G}
+ *                 (q[e][n][c] - 8) * x[perm[j] / k][c],   e = e(j).
+ *
+ *   q         [N_r, n_out, d/2] bytes: column 2i in the low nibble of byte i,
+ *             column 2i+1 in the high one; nibble u stands for u - 8.
+ *   scales    [N_r, n_out, ceil(d / group)] of scale_dtype (MR_BF16 or MR_F32).
+ *   packed    the layout the kernel streams (16 x 128 blocks in the order the
+ *             tensor core's lanes read them, then the scales in their own
+ *             type), mr_expert_w4_packed_bytes bytes, caller-owned, 16-byte
+ *             aligned; written once, when the weights are loaded.
+ *   x, perm, offsets, out   as mr_expert_gemm_gather (perm NULL: x holds the
+ *             sorted rows); rows of out from offsets[N_r] on are not written.
+ * x times the 4-bit integers is exact in fp32; each group's fp32 sum is scaled
+ * and added in fp32, and the result rounded to bf16 once.  One kernel, no
+ * workspace, a fixed order of sums.  Any number of tokens is right; an expert's
+ * weights are read again for every 16 of its rows, so larger batches are
+ * better served by mr_expert_gemm_gather.
+ * mr_expert_w4_packed_bytes returns 0 for arguments it does not know.
+ * Limits: group 32, 64 or 128, d % 8 == 0, N_r <= 1024, N_r * n_out < 2^31,
+ * 16-byte aligned x (else MR_ERR_UNSUPPORTED).
+ */
+size_t mr_expert_w4_packed_bytes(int N_r, int n_out, int d, int group,
+                                 int scale_dtype);
+int mr_expert_pack_w4(const void *q, const void *scales, int scale_dtype,
+                      int N_r, int n_out, int d, int group, void *packed,
+                      size_t packed_bytes, mr_stream_t stream);
+int mr_expert_gemv_gather_w4(const void *x, const int32_t *perm,
+                             const int32_t *offsets, const void *packed,
+                             int scale_dtype, int T, int d, int k, int N_r,
+                             int n_out, int group, void *out,
+                             mr_stream_t stream);
+
+/*
  * mr_launch_count -- number of kernels this library has launched in this
  * process (all devices and streams), for accounting in benchmarks.
  */

@@ -87,6 +87,16 @@ def lib():
         L.mr_expert_packed_bytes.restype = sz
         L.mr_expert_pack_weights.argtypes = [p, i, i, i, p, sz, p]
         L.mr_combine.argtypes = [p, i, p, p, p, p, i, i, i, p]
+        L.mr_combine_backward.argtypes = [p, i, p, p, p, i, i, i, p, p, p]
+        L.mr_gather_rows_backward.argtypes = [p, i, p, p, i, i, i, p, p]
+        L.mr_router_backward_workspace_size.argtypes = [i, i, i, i, i]
+        L.mr_router_backward_workspace_size.restype = sz
+        L.mr_router_backward.argtypes = [p, i, p, i, p, p, p, p, p, i, i, i, i, f, i, p, p, p, p,
+                                         p, sz, p]
+        L.mr_expert_w4_packed_bytes.argtypes = [i, i, i, i, i]
+        L.mr_expert_w4_packed_bytes.restype = sz
+        L.mr_expert_pack_w4.argtypes = [p, p, i, i, i, i, i, p, sz, p]
+        L.mr_expert_gemv_gather_w4.argtypes = [p, p, p, p, i, i, i, i, i, i, i, p, p]
         L.mr_ep_dispatch_p2p.argtypes = [p, i, i, i, i, p, p, p, p, i, i, i, p, i, p, p, p, p]
         L.mr_ep_combine_p2p.argtypes = [p, i, i, p, p, p, i, i, i, p, p, i, i, p]
         L.mr_ipc_export.argtypes = [p, sz, C.POINTER(_IpcHandle)]
@@ -466,6 +476,161 @@ def mr_combine(expert_out, w, inv_perm, shared=None, y=None, stream=None):
     _call("mr_combine", _device_of(expert_out, w, inv_perm, shared, y), stream,
           _ptr(expert_out), dt, _ptr(w), _ptr(inv_perm), _ptr(shared), _ptr(y), T, d, k)
     return y
+
+
+def mr_combine_backward(dy, expert_out, w, inv_perm, dexpert=None, dw=None, want_dexpert=True,
+                        want_dw=True, stream=None):
+    """Gradients of mr_combine from dy [T,d]: (dexpert [T*k,d] in dy's dtype,
+    dw [T,k] fp32), None for one that is not wanted (want_dexpert / want_dw
+    False and no buffer given).  expert_out [T*k,d] may be None without dw.
+    The shared row's gradient is dy itself."""
+    _need(w, "w", torch.float32)
+    T, k = w.shape
+    _need(dy, "dy")
+    dt = _row_dtype(dy)
+    d = dy.shape[-1]
+    _need(dy, "dy", None, (T, d))
+    _need(inv_perm, "inv_perm", torch.int32, (T * k,))
+    if expert_out is not None:
+        _need(expert_out, "expert_out", dy.dtype, (T * k, d))
+    if dexpert is not None:
+        _need(dexpert, "dexpert", dy.dtype, (T * k, d))
+    elif want_dexpert:
+        dexpert = torch.empty((T * k, d), dtype=dy.dtype, device=dy.device)
+    if dw is not None:
+        _need(dw, "dw", torch.float32, (T, k))
+    elif want_dw:
+        dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    if dw is not None and expert_out is None:
+        raise ValueError("dw needs expert_out")
+    _call("mr_combine_backward", _device_of(dy, expert_out, w, inv_perm, dexpert, dw), stream,
+          _ptr(dy), dt, _ptr(expert_out), _ptr(w), _ptr(inv_perm), T, d, k, _ptr(dexpert),
+          _ptr(dw))
+    return dexpert, dw
+
+
+def mr_gather_rows_backward(dxs, k, inv_perm, add=None, dx=None, stream=None):
+    """Gradient of mr_gather_rows: dx [T,d] = the sum of each token's k rows of
+    dxs [T*k,d] (+ add [T,d]), summed in fp32 and rounded once."""
+    _need(dxs, "dxs")
+    dt = _row_dtype(dxs)
+    rows, d = dxs.shape
+    if k <= 0 or rows % k:
+        raise ValueError(f"dxs has {rows} rows, not a multiple of k = {k}")
+    T = rows // k
+    _need(inv_perm, "inv_perm", torch.int32, (T * k,))
+    if add is not None:
+        _need(add, "add", dxs.dtype, (T, d))
+    dx = torch.empty((T, d), dtype=dxs.dtype, device=dxs.device) if dx is None else \
+        _need(dx, "dx", dxs.dtype, (T, d))
+    _call("mr_gather_rows_backward", _device_of(dxs, inv_perm, add, dx), stream, _ptr(dxs), dt,
+          _ptr(inv_perm), _ptr(add), T, d, k, _ptr(dx))
+    return dx
+
+
+def mr_router_backward_workspace_size(T, d, N_r, k, flags=0) -> int:
+    return int(lib().mr_router_backward_workspace_size(T, d, N_r, k, flags))
+
+
+def mr_router_backward(x, W, logits, idx, dw, perm, offsets, route_scale, flags=0, add=None,
+                       dlogits=None, dx=None, dW=None, want_dx=True, want_dW=True,
+                       workspace=None, stream=None):
+    """Gradient of the gate from dw [T,k] (the router weights' gradient):
+    (dx [T,d] in x's dtype, dW [N_r,d] fp32), None for one that is not wanted
+    (want_dx / want_dW False and no buffer given).  x [T,d], W [N_r,d] fp32 or
+    bf16, logits [T,N_r] fp32 (the forward's logits_out), idx [T,k]; perm [T*k]
+    and offsets [N_r+1] from mr_dispatch of idx (None allowed with softmax
+    scores or without dW).  flags as in the forward; add [T,d] joins dx;
+    dlogits: optional [T,N_r] fp32 output."""
+    _need(x, "x")
+    x_dtype = _row_dtype(x)
+    T, d = x.shape
+    _need(W, "W")
+    W_dtype = _row_dtype(W)
+    N_r = W.shape[0]
+    _need(W, "W", None, (N_r, d))
+    _need(logits, "logits", torch.float32, (T, N_r))
+    _need(idx, "idx", torch.int32)
+    k = idx.shape[1]
+    _need(idx, "idx", torch.int32, (T, k))
+    _need(dw, "dw", torch.float32, (T, k))
+    if perm is not None:
+        _need(perm, "perm", torch.int32, (T * k,))
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, (N_r + 1,))
+    if add is not None:
+        _need(add, "add", x.dtype, (T, d))
+    if dlogits is not None:
+        _need(dlogits, "dlogits", torch.float32, (T, N_r))
+    if dx is not None:
+        _need(dx, "dx", x.dtype, (T, d))
+    elif want_dx:
+        dx = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if dW is not None:
+        _need(dW, "dW", torch.float32, (N_r, d))
+    elif want_dW:
+        dW = torch.empty((N_r, d), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(mr_router_backward_workspace_size(T, d, N_r, k, flags), 16),
+                                dtype=torch.uint8, device=x.device)
+    _need(workspace, "workspace")
+    _call("mr_router_backward", _device_of(x, W, logits, idx, dw, perm, offsets, add, dlogits, dx,
+                                           dW, workspace), stream,
+          _ptr(x), x_dtype, _ptr(W), W_dtype, _ptr(logits), _ptr(idx), _ptr(dw), _ptr(perm),
+          _ptr(offsets), T, d, N_r, k, float(route_scale), int(flags), _ptr(add), _ptr(dlogits),
+          _ptr(dx), _ptr(dW), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return dx, dW
+
+
+def mr_expert_pack_w4(q, scales, group, stream=None):
+    """4-bit expert weights q [N_r, n_out, d/2] uint8 (column 2i in the low
+    nibble of byte i; nibble u stands for u - 8) and scales [N_r, n_out,
+    ceil(d/group)] (bf16 or fp32) -> the packed layout (flat uint8) that
+    mr_expert_gemv_gather_w4 reads."""
+    _need(q, "q", torch.uint8)
+    N_r, n_out, half = q.shape
+    d = 2 * half
+    _need(scales, "scales")
+    sdt = _row_dtype(scales)
+    n = int(lib().mr_expert_w4_packed_bytes(N_r, n_out, d, group, sdt))
+    if n == 0:
+        raise MRError("mr_expert_pack_w4", MR_ERR_UNSUPPORTED)
+    _need(scales, "scales", None, (N_r, n_out, -(-d // group)))
+    packed = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _call("mr_expert_pack_w4", _device_of(q, scales, packed), stream, _ptr(q), _ptr(scales), sdt,
+          N_r, n_out, d, group, _ptr(packed), n)
+    return packed
+
+
+def mr_expert_gemv_gather_w4(x, k, perm, offsets, packed, N_r, n_out, group,
+                             scale_dtype=torch.bfloat16, out=None, stream=None):
+    """mr_expert_gemm_gather on 4-bit weights for few tokens: out [T*k, n_out]
+    bf16 from x [T,d] bf16 (perm None: x holds the sorted rows) and `packed`
+    (mr_expert_pack_w4 with the same group and scale type)."""
+    _need(x, "x", torch.bfloat16)
+    T, d = x.shape
+    if perm is None:
+        if T % k:
+            raise ValueError("without perm, x must have T*k rows")
+        T //= k
+    else:
+        _need(perm, "perm", torch.int32, (T * k,))
+    _need(offsets, "offsets", torch.int32, (N_r + 1,))
+    _need(packed, "packed", torch.uint8)
+    sdt = MR_BF16 if scale_dtype == torch.bfloat16 else MR_F32 if scale_dtype == torch.float32 \
+        else None
+    if sdt is None:
+        raise TypeError("scales must be bfloat16 or float32")
+    n = int(lib().mr_expert_w4_packed_bytes(N_r, n_out, d, group, sdt))
+    if n == 0:
+        raise MRError("mr_expert_gemv_gather_w4", MR_ERR_UNSUPPORTED)
+    if packed.numel() != n:
+        raise ValueError(f"packed has {packed.numel()} bytes, these sizes need {n}")
+    out = torch.empty((T * k, n_out), dtype=torch.bfloat16, device=x.device) if out is None \
+        else _need(out, "out", torch.bfloat16, (T * k, n_out))
+    _call("mr_expert_gemv_gather_w4", _device_of(x, perm, offsets, packed, out), stream, _ptr(x),
+          _ptr(perm), _ptr(offsets), _ptr(packed), sdt, T, d, k, N_r, n_out, group, _ptr(out))
+    return out
 
 
 def _addresses(bufs, name, dev):

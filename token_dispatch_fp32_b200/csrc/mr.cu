@@ -15,13 +15,16 @@
 #include "dispatch.cuh"
 #include "ep.cuh"
 #include "expert_gemm.cuh"
+#include "expert_w4.cuh"
 #include "mr_common.cuh"
+#include "router_backward.cuh"
 #include "router_ffma.cuh"
 #include "router_splitk.cuh"
 #include "router_tc.cuh"
 #include "route.cuh"
 #include "combine.cuh"
 #include "gather.cuh"
+#include "rows_backward.cuh"
 
 namespace {
 
@@ -1388,6 +1391,373 @@ int mr_combine(const void* expert_out, int dtype, const float* w, const int32_t*
                                 return mr::SlotRowsLocal<const V>{
                                     static_cast<const V*>(expert_out), inv_perm};
                               });
+}
+
+}  // extern "C"
+
+// ---- gradients of the path -----------------------------------------------------
+
+namespace {
+
+template <typename V, bool BF16>
+int launch_combine_backward(const void* dy, const void* E, const float* w, const int32_t* inv,
+                            void* dE, float* dw, int T, long nvec, int k, cudaStream_t s) {
+  mr::combine_backward_kernel<V, BF16><<<(unsigned)T, mr::kRowThreads, 0, s>>>(
+      static_cast<const V*>(dy), static_cast<const V*>(E), w, inv, static_cast<V*>(dE), dw, nvec,
+      k);
+  return launch_status();
+}
+
+template <typename V, bool BF16>
+int launch_gather_backward(const void* dxs, const int32_t* inv, const void* add, void* dx, int T,
+                           long nvec, int k, unsigned grid, cudaStream_t s) {
+  mr::gather_backward_kernel<V, BF16><<<grid, mr::kRowThreads, 0, s>>>(
+      static_cast<const V*>(dxs), inv, static_cast<const V*>(add), static_cast<V*>(dx), T, nvec,
+      k);
+  return launch_status();
+}
+
+// Workspace of mr_router_backward: the slots' logit gradients, softmax's dense
+// ones, and dW's partial sums (extra pieces of long segments, or K slices).
+struct RouterBwdWs {
+  size_t slot, dense, part, total;
+  int slices;  // K slices of the dense dW product (softmax)
+};
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+RouterBwdWs router_bwd_ws(int T, int d, int N_r, int k, int flags) {
+  RouterBwdWs w;
+  w.slices = 0;
+  w.slot = 0;
+  size_t at = align256((size_t)T * k * sizeof(float));
+  w.dense = at;
+  if (flags & MR_SCORE_SOFTMAX) {
+    at += align256((size_t)T * N_r * sizeof(float));
+    // slices of at least 512 tokens, up to about four tiles per SM
+    const long tiles = (long)((N_r + mr::rb::kGemmT - 1) / mr::rb::kGemmT) *
+                       ((d + mr::rb::kGemmT - 1) / mr::rb::kGemmT);
+    long z = (4 * 148 + tiles - 1) / tiles;
+    z = std::min<long>(z, T / 512);
+    w.slices = (int)std::max<long>(1, z);
+    w.part = at;
+    if (w.slices > 1) at += (size_t)w.slices * N_r * d * sizeof(float);
+  } else {
+    w.part = at;
+    at += (size_t)((long)T * k / mr::rb::kDwRows) * d * sizeof(float);
+  }
+  w.total = at;
+  return w;
+}
+
+template <int CPL, bool VEC, bool BF16, bool WBF16>
+int launch_dx_slots(const void* W, const int32_t* idx, const float* slot, const void* add,
+                    void* dx, int T, int d, int N_r, int k, int sms, cudaStream_t s) {
+  constexpr int CW = 32 * CPL;
+  auto kern = mr::rb::dx_slots_kernel<CPL, VEC, BF16, WBF16>;
+  const size_t smem = (size_t)(N_r + 1) * CW * sizeof(float) + mr::rb::kDxPairs * sizeof(int2);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return MR_ERR_CUDA;
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, mr::rb::kDxThreads, smem) !=
+          cudaSuccess ||
+      per_sm < 1)
+    return MR_ERR_CUDA;
+  // token ranges per column chunk: whole waves of resident CTAs, at least 64
+  // tokens each (a CTA first loads N_r * CW weights)
+  const int chunks = (d + CW - 1) / CW;
+  const long slots = (long)sms * per_sm;
+  long split = std::max<long>(1, slots * 2 / chunks);
+  split = std::min<long>(split, (T + 63) / 64);
+  const int per_cta = (int)((T + split - 1) / split);
+  const unsigned gy = (unsigned)((T + per_cta - 1) / per_cta);
+  kern<<<dim3((unsigned)chunks, gy), mr::rb::kDxThreads, smem, s>>>(W, idx, slot, add, dx, T, d,
+                                                                     N_r, k, per_cta);
+  return launch_status();
+}
+
+template <bool BF16, bool WBF16>
+int launch_dx(const void* W, const int32_t* idx, const float* slot, const void* add, void* dx,
+              int T, int d, int N_r, int k, int sms, cudaStream_t s) {
+  const bool vec = d % 4 == 0 && aligned16(dx) && (!add || aligned16(add));
+  // 128 columns of every expert when they fit shared memory (N_r <= 432), else 64
+  if (((size_t)N_r + 1) * 128 * sizeof(float) + mr::rb::kDxPairs * sizeof(int2) <= 232448) {
+    if (vec)
+      return launch_dx_slots<4, true, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+    return launch_dx_slots<4, false, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+  }
+  if (vec)
+    return launch_dx_slots<2, true, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+  return launch_dx_slots<2, false, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+}
+
+template <typename V, bool BF16>
+int launch_dw_slots(const void* x, const int32_t* perm, const int32_t* offsets, const float* slot,
+                    int n, int N_r, int k, long nvec, float* dW, float* part, cudaStream_t s) {
+  const unsigned pieces = (unsigned)((n + mr::rb::kDwRows - 1) / mr::rb::kDwRows + N_r);
+  const unsigned slabs = (unsigned)((nvec + mr::rb::kDwThreads - 1) / mr::rb::kDwThreads);
+  mr::rb::dw_slots_kernel<V, BF16><<<dim3(pieces, slabs), mr::rb::kDwThreads, 0, s>>>(
+      static_cast<const V*>(x), perm, offsets, slot, n, N_r, k, nvec, dW, part);
+  return launch_status();
+}
+
+// C = A . B on the CUDA cores (mr::rb::dense_kernel).
+template <bool TA>
+int launch_dense(const float* A, const void* B, bool b_bf16, const void* add, void* C,
+                 bool out_bf16, int M, int N, int K, int slices, cudaStream_t s) {
+  const dim3 grid((unsigned)((N + mr::rb::kGemmT - 1) / mr::rb::kGemmT),
+                  (unsigned)((M + mr::rb::kGemmT - 1) / mr::rb::kGemmT), (unsigned)slices);
+  if (out_bf16) {
+    if (b_bf16) mr::rb::dense_kernel<TA, true, true><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);
+    else mr::rb::dense_kernel<TA, false, true><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);
+  } else {
+    if (b_bf16) mr::rb::dense_kernel<TA, true, false><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);
+    else mr::rb::dense_kernel<TA, false, false><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mr_combine_backward(const void* dy, int dtype, const void* expert_out, const float* w,
+                        const int32_t* inv_perm, int T, int d, int k, void* dexpert, float* dw,
+                        mr_stream_t stream) {
+  if (T < 0 || d <= 0 || k <= 0 || (dtype != MR_F32 && dtype != MR_BF16)) return MR_ERR_INVALID_ARG;
+  if ((long long)T * k >= (1LL << 31)) return MR_ERR_INVALID_ARG;
+  if (k > mr::kRowMaxK) return MR_ERR_UNSUPPORTED;
+  if (T == 0) return MR_OK;
+  if (!dy || !w || !inv_perm || (!dexpert && !dw) || (dw && !expert_out))
+    return MR_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const void* E = dw ? expert_out : nullptr;  // only the weights' gradient reads the rows
+  const bool bf16 = dtype == MR_BF16;
+  const long row_bytes = (long)d * (bf16 ? 2 : 4);
+  auto all = [&](bool (*ok)(const void*)) { return ok(dy) && (!E || ok(E)) && (!dexpert || ok(dexpert)); };
+  if (row_bytes % 32 == 0 && all(aligned32)) {
+    return bf16 ? launch_combine_backward<mr::Vec32, true>(dy, E, w, inv_perm, dexpert, dw, T,
+                                                           row_bytes / 32, k, s)
+                : launch_combine_backward<mr::Vec32, false>(dy, E, w, inv_perm, dexpert, dw, T,
+                                                            row_bytes / 32, k, s);
+  }
+  if (row_bytes % 16 == 0 && all(aligned16)) {
+    return bf16 ? launch_combine_backward<uint4, true>(dy, E, w, inv_perm, dexpert, dw, T,
+                                                       row_bytes / 16, k, s)
+                : launch_combine_backward<uint4, false>(dy, E, w, inv_perm, dexpert, dw, T,
+                                                        row_bytes / 16, k, s);
+  }
+  return bf16 ? launch_combine_backward<uint16_t, true>(dy, E, w, inv_perm, dexpert, dw, T, d, k, s)
+              : launch_combine_backward<float, false>(dy, E, w, inv_perm, dexpert, dw, T, d, k, s);
+}
+
+int mr_gather_rows_backward(const void* dxs, int dtype, const int32_t* inv_perm, const void* add,
+                            int T, int d, int k, void* dx, mr_stream_t stream) {
+  if (T < 0 || d <= 0 || k <= 0 || (dtype != MR_F32 && dtype != MR_BF16)) return MR_ERR_INVALID_ARG;
+  if ((long long)T * k >= (1LL << 31)) return MR_ERR_INVALID_ARG;
+  if (k > mr::kRowMaxK) return MR_ERR_UNSUPPORTED;
+  if (T == 0) return MR_OK;
+  if (!dxs || !inv_perm || !dx) return MR_ERR_INVALID_ARG;
+  int sms = 0, cc = 0;
+  if (!device_info(&sms, &cc)) return MR_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == MR_BF16;
+  const long row_bytes = (long)d * (bf16 ? 2 : 4);
+  auto all = [&](bool (*ok)(const void*)) { return ok(dxs) && ok(dx) && (!add || ok(add)); };
+  const unsigned grid = (unsigned)std::min<long>(T, (long)sms * 16);
+  if (row_bytes % 32 == 0 && all(aligned32))
+    return bf16 ? launch_gather_backward<mr::Vec32, true>(dxs, inv_perm, add, dx, T,
+                                                          row_bytes / 32, k, grid, s)
+                : launch_gather_backward<mr::Vec32, false>(dxs, inv_perm, add, dx, T,
+                                                           row_bytes / 32, k, grid, s);
+  if (row_bytes % 16 == 0 && all(aligned16))
+    return bf16 ? launch_gather_backward<uint4, true>(dxs, inv_perm, add, dx, T, row_bytes / 16, k,
+                                                      grid, s)
+                : launch_gather_backward<uint4, false>(dxs, inv_perm, add, dx, T, row_bytes / 16,
+                                                       k, grid, s);
+  return bf16 ? launch_gather_backward<uint16_t, true>(dxs, inv_perm, add, dx, T, d, k, grid, s)
+              : launch_gather_backward<float, false>(dxs, inv_perm, add, dx, T, d, k, grid, s);
+}
+
+size_t mr_router_backward_workspace_size(int T, int d, int N_r, int k, int flags) {
+  if (T <= 0 || d <= 0 || N_r <= 0 || k <= 0) return 0;
+  return router_bwd_ws(T, d, N_r, k, flags).total;
+}
+
+int mr_router_backward(const void* x, int x_dtype, const void* W, int W_dtype,
+                       const float* logits, const int32_t* idx, const float* dw,
+                       const int32_t* perm, const int32_t* offsets, int T, int d, int N_r, int k,
+                       float route_scale, int flags, const void* add, float* dlogits, void* dx,
+                       float* dW, void* workspace, size_t workspace_bytes, mr_stream_t stream) {
+  if (T < 0 || d <= 0 || N_r <= 0 || k <= 0) return MR_ERR_INVALID_ARG;
+  if ((x_dtype != MR_F32 && x_dtype != MR_BF16) || (W_dtype != MR_F32 && W_dtype != MR_BF16))
+    return MR_ERR_INVALID_ARG;
+  if (flags & ~(MR_SCORE_SOFTMAX | MR_GROUP_MAX | MR_NORM_NO_EPS)) return MR_ERR_INVALID_ARG;
+  if (!std::isfinite(route_scale)) return MR_ERR_INVALID_ARG;
+  if ((long long)T * k >= (1LL << 31) || (long long)T * d >= (1LL << 40)) return MR_ERR_INVALID_ARG;
+  if (N_r > mr::rb::kMaxN || k > mr::rb::kMaxK) return MR_ERR_UNSUPPORTED;
+  if (!dlogits && !dx && !dW) return MR_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (dW && cudaMemsetAsync(dW, 0, (size_t)N_r * d * sizeof(float), s) != cudaSuccess)
+      return MR_ERR_CUDA;
+    return MR_OK;
+  }
+  const bool softmax = (flags & MR_SCORE_SOFTMAX) != 0;
+  if (!logits || !idx || !dw || !workspace || (dx && !W) || (dW && !x) ||
+      (dW && !softmax && (!perm || !offsets)))
+    return MR_ERR_INVALID_ARG;
+  const RouterBwdWs ws = router_bwd_ws(T, d, N_r, k, flags);
+  if (workspace_bytes < ws.total || !aligned16(workspace)) return MR_ERR_INVALID_ARG;
+  int sms = 0, cc = 0;
+  if (!device_info(&sms, &cc)) return MR_ERR_CUDA;
+  char* base = static_cast<char*>(workspace);
+  float* slot = reinterpret_cast<float*>(base + ws.slot);
+  float* dense = dlogits ? dlogits : softmax ? reinterpret_cast<float*>(base + ws.dense) : nullptr;
+  float* part = reinterpret_cast<float*>(base + ws.part);
+  const float eps = (flags & MR_NORM_NO_EPS) ? 0.0f : mr::rb::kEps;
+  const unsigned gt = (unsigned)((T + mr::rb::kDlWarps - 1) / mr::rb::kDlWarps);
+  if (softmax)
+    mr::rb::dlogits_kernel<true><<<gt, 32 * mr::rb::kDlWarps, 0, s>>>(
+        logits, idx, dw, T, N_r, k, route_scale, eps, slot, dense);
+  else
+    mr::rb::dlogits_kernel<false><<<gt, 32 * mr::rb::kDlWarps, 0, s>>>(
+        logits, idx, dw, T, N_r, k, route_scale, eps, slot, dense);
+  int rc = launch_status();
+  if (rc != MR_OK) return rc;
+  const bool xb = x_dtype == MR_BF16, wb = W_dtype == MR_BF16;
+  if (dx) {
+    if (softmax) rc = launch_dense<false>(dense, W, wb, add, dx, xb, T, d, N_r, 1, s);
+    else if (xb)
+      rc = wb ? launch_dx<true, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
+              : launch_dx<true, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+    else
+      rc = wb ? launch_dx<false, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
+              : launch_dx<false, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+    if (rc != MR_OK) return rc;
+  }
+  if (dW && softmax) {
+    rc = launch_dense<true>(dense, x, xb, nullptr, ws.slices > 1 ? part : dW, false, N_r, d, T,
+                            ws.slices, s);
+    if (rc != MR_OK || ws.slices <= 1) return rc;
+    const long n = (long)N_r * d;
+    const unsigned grid = (unsigned)std::min<long>((n + 255) / 256, (long)sms * 16);
+    mr::rb::sum_slices_kernel<<<grid, 256, 0, s>>>(part, ws.slices, n, dW);
+    return launch_status();
+  }
+  if (dW) {
+    const int n = T * k;
+    const bool vec = aligned16(x) && d % (xb ? 8 : 4) == 0;
+    if (vec)
+      rc = xb ? launch_dw_slots<uint4, true>(x, perm, offsets, slot, n, N_r, k, d / 8, dW, part, s)
+              : launch_dw_slots<uint4, false>(x, perm, offsets, slot, n, N_r, k, d / 4, dW, part, s);
+    else
+      rc = xb ? launch_dw_slots<uint16_t, true>(x, perm, offsets, slot, n, N_r, k, d, dW, part, s)
+              : launch_dw_slots<float, false>(x, perm, offsets, slot, n, N_r, k, d, dW, part, s);
+    if (rc != MR_OK) return rc;
+    mr::rb::dw_join_kernel<<<dim3((unsigned)N_r, (unsigned)((d + 1023) / 1024)), 256, 0, s>>>(
+        offsets, n, N_r, d, part, dW);
+    return launch_status();
+  }
+  return MR_OK;
+}
+
+// ---- experts on 4-bit weights ---------------------------------------------------
+
+size_t mr_expert_w4_packed_bytes(int N_r, int n_out, int d, int group, int scale_dtype) {
+  if (N_r <= 0 || n_out <= 0 || d <= 0 || (group != 32 && group != 64 && group != 128) ||
+      (scale_dtype != MR_F32 && scale_dtype != MR_BF16))
+    return 0;
+  return mr::w4::make_layout(N_r, n_out, d, group, scale_dtype == MR_BF16 ? 2 : 4).total;
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_w4(int N_r, int n_out, int d, int group, int scale_dtype) {
+  if (N_r <= 0 || n_out <= 0 || d <= 0 || (scale_dtype != MR_F32 && scale_dtype != MR_BF16))
+    return MR_ERR_INVALID_ARG;
+  if ((long long)N_r * n_out >= (1LL << 31)) return MR_ERR_INVALID_ARG;
+  if ((group != 32 && group != 64 && group != 128) || d % 8 != 0 || N_r > mr::kDispMaxExperts)
+    return MR_ERR_UNSUPPORTED;
+  return MR_OK;
+}
+
+template <int GROUP, typename S>
+int launch_expert_w4(const mr::w4::Params& P, dim3 grid, cudaStream_t s) {
+  mr::w4::expert_w4_kernel<GROUP, S><<<grid, mr::w4::kThreads, 0, s>>>(P);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mr_expert_pack_w4(const void* q, const void* scales, int scale_dtype, int N_r, int n_out,
+                      int d, int group, void* packed, size_t packed_bytes, mr_stream_t stream) {
+  const int rc = check_w4(N_r, n_out, d, group, scale_dtype);
+  if (rc != MR_OK) return rc;
+  const int sb = scale_dtype == MR_BF16 ? 2 : 4;
+  const mr::w4::Layout l = mr::w4::make_layout(N_r, n_out, d, group, sb);
+  if (!q || !scales || !packed || packed_bytes < l.total) return MR_ERR_INVALID_ARG;
+  if (!aligned16(packed)) return MR_ERR_UNSUPPORTED;
+  const long ctas = (l.blocks + 7) / 8;
+  if (ctas >= (1LL << 31)) return MR_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint4* wp = static_cast<uint4*>(packed);
+  void* sp = static_cast<char*>(packed) + l.scale_off;
+  if (sb == 2)
+    mr::w4::w4_pack_kernel<uint16_t><<<(unsigned)ctas, 256, 0, s>>>(
+        static_cast<const uint8_t*>(q), static_cast<const uint16_t*>(scales), n_out, d, group,
+        l.MT, l.KB, l.blocks, wp, static_cast<uint16_t*>(sp));
+  else
+    mr::w4::w4_pack_kernel<float><<<(unsigned)ctas, 256, 0, s>>>(
+        static_cast<const uint8_t*>(q), static_cast<const float*>(scales), n_out, d, group, l.MT,
+        l.KB, l.blocks, wp, static_cast<float*>(sp));
+  return launch_status();
+}
+
+int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* offsets,
+                             const void* packed, int scale_dtype, int T, int d, int k, int N_r,
+                             int n_out, int group, void* out, mr_stream_t stream) {
+  if (T < 0 || k <= 0 || (long long)T * k >= (1LL << 31)) return MR_ERR_INVALID_ARG;
+  const int rc = check_w4(N_r, n_out, d, group, scale_dtype);
+  if (rc != MR_OK) return rc;
+  if (T == 0) return MR_OK;
+  if (!x || !offsets || !packed || !out) return MR_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(packed)) return MR_ERR_UNSUPPORTED;
+  const int sb = scale_dtype == MR_BF16 ? 2 : 4;
+  const mr::w4::Layout l = mr::w4::make_layout(N_r, n_out, d, group, sb);
+  mr::w4::Params P;
+  P.x = static_cast<const uint16_t*>(x);
+  P.perm = perm;
+  P.offsets = offsets;
+  P.wp = static_cast<const uint4*>(packed);
+  P.sp = static_cast<const char*>(packed) + l.scale_off;
+  P.out = static_cast<uint16_t*>(out);
+  P.T = T;
+  P.d = d;
+  P.k = k;
+  P.N_r = N_r;
+  P.n_out = n_out;
+  P.MT = l.MT;
+  P.KB = l.KB;
+  // fewer sorted rows than experts: count the rows, so that one token does not
+  // launch a CTA for every expert it did not choose
+  P.rows_mode = (long)T * k < N_r ? 1 : 0;
+  const dim3 grid((unsigned)((l.MT + mr::w4::kMT - 1) / mr::w4::kMT),
+                  (unsigned)(P.rows_mode ? T * k : N_r));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (sb == 2) {
+    if (group == 32) return launch_expert_w4<32, uint16_t>(P, grid, s);
+    if (group == 64) return launch_expert_w4<64, uint16_t>(P, grid, s);
+    return launch_expert_w4<128, uint16_t>(P, grid, s);
+  }
+  if (group == 32) return launch_expert_w4<32, float>(P, grid, s);
+  if (group == 64) return launch_expert_w4<64, float>(P, grid, s);
+  return launch_expert_w4<128, float>(P, grid, s);
 }
 
 // ---- expert parallelism over peer memory ------------------------------------

@@ -1,0 +1,493 @@
+// router_backward.cuh -- gradient of the gate (router_tc.cuh, route.cuh,
+// router_splitk.cuh): from the router weights' gradient g = dw [T,k] to the
+// hidden states and the gate weight.
+//
+// Forward of token t (Kimi K2 "Normalize weights" page, MoEGate.forward;
+// DeepSeek-V3.2-Exp "Normalize weights" page, Gate.forward): L = x . W^T,
+// s = sigmoid(L) or softmax(L), w_j = scale * s_j / (S + eps), S = sum_j s_j
+// (softmax: w_j = scale * s_j).  The choice of experts is piecewise constant
+// and the bias only enters the choice, so neither has a gradient:
+//   sigmoid: dl_j = scale/(S+eps) * (g_j - sum_i g_i s_i / (S+eps)) * s_j (1 - s_j)
+//            on the k chosen logits, 0 elsewhere;
+//   softmax: dL_i = scale * s_i * ([i chosen] g_i - sum_j g_j s_j), every i.
+//   dx = dL . W (+ add),  dW = dL^T . x.
+// With sigmoid scores dL has k of N_r entries per token: dx sums k rows of W,
+// dW[e] sums the rows of the tokens that chose e, which mr_dispatch's
+// permutation lists.  Softmax makes both dense products.
+#pragma once
+
+#include "combine.cuh"
+#include "mr_common.cuh"
+#include "rows_backward.cuh"
+
+namespace mr {
+namespace rb {
+
+constexpr float kEps = 1e-20f;
+constexpr int kMaxK = 32;
+constexpr int kMaxN = 512;
+
+// sigmoid(L) and 1 - sigmoid(L), each to full relative accuracy.
+__device__ __forceinline__ void sigmoid_pair(float L, float& s, float& c) {
+  const float q = expf(-fabsf(L));
+  const float r = 1.0f / (1.0f + q);
+  s = L >= 0.0f ? r : q * r;
+  c = L >= 0.0f ? q * r : r;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// One warp per token.  Sigmoid: slot[t*k + j] = dl_j (0 for an id outside
+// [0, N_r)); `dense` (optional) gets the whole row dL[t].  Softmax: `dense`
+// is required and slot is not written.
+constexpr int kDlWarps = 4;
+template <bool SOFTMAX>
+__global__ void __launch_bounds__(32 * kDlWarps)
+    dlogits_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                   const float* __restrict__ g, int T, int N_r, int k, float scale, float eps,
+                   float* __restrict__ slot, float* __restrict__ dense) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long t = (long)blockIdx.x * kDlWarps + warp;
+  if (t >= T) return;
+  const float* L = logits + t * N_r;
+  const int e = lane < k ? idx[t * k + lane] : -1;
+  const bool ok = e >= 0 && e < N_r;
+  if (lane < k && !ok) mr_raise(MR_FLAG_BAD_INDEX);
+  const float gj = ok ? g[t * k + lane] : 0.0f;
+  if constexpr (!SOFTMAX) {
+    float s = 0.0f, c = 0.0f;
+    if (ok) sigmoid_pair(L[e], s, c);
+    const float inv = 1.0f / (warp_sum(s) + eps);
+    const float mean = warp_sum(gj * s) * inv;
+    const float dl = ok ? scale * inv * (gj - mean) * (s * c) : 0.0f;
+    if (lane < k) slot[t * k + lane] = dl;
+    if (dense) {
+      for (int i = lane; i < N_r; i += 32) dense[t * N_r + i] = 0.0f;
+      __syncwarp();
+      for (int j = 0; j < k; ++j) {  // one after the other: an id may repeat
+        if (lane == j && ok) dense[t * N_r + e] += dl;
+        __syncwarp();
+      }
+    }
+  } else {
+    float mx = -INFINITY;
+    for (int i = lane; i < N_r; i += 32) mx = fmaxf(mx, L[i]);
+    mx = warp_max(mx);
+    float sum = 0.0f;
+    for (int i = lane; i < N_r; i += 32) sum += expf(L[i] - mx);
+    const float inv = 1.0f / warp_sum(sum);
+    const float pj = ok ? expf(L[e] - mx) * inv : 0.0f;
+    const float mean = warp_sum(gj * pj);
+    // a chosen entry is scale * p * (sum of its slots' g - mean); its own sum
+    // first, then the difference, so no two large terms cancel late
+    float gs = gj;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(0xffffffffu, e, j);
+      const float gg = __shfl_sync(0xffffffffu, gj, j);
+      if (ok && j != lane && ej == e) gs += gg;
+    }
+    for (int i = lane; i < N_r; i += 32)
+      dense[t * N_r + i] = -scale * (expf(L[i] - mx) * inv) * mean;
+    __syncwarp();
+    if (ok) dense[t * N_r + e] = scale * pj * (gs - mean);  // equal ids write equal values
+  }
+}
+
+// ---- sigmoid: dx[t] = sum_j dl[t,j] * W[idx[t,j]] (+ add[t]) ------------------
+//
+// A CTA keeps CW = 32 * CPL columns of every expert's row of W (fp32, plus one
+// row of zeros for ids out of range) in shared memory and walks a range of
+// tokens, one warp per token (addv may be dxv: neither is __restrict__): each slot is one conflict-free read of its
+// expert's CW columns and CPL fused multiply-adds per lane.  The k * d reads
+// of W per token then come from shared memory (128 bytes a cycle and SM)
+// instead of L2, which is what bounds the kernel.  The tokens' (row, dl) pairs
+// are staged kDxBatch tokens at a time.
+constexpr int kDxThreads = 512;
+constexpr int kDxPairs = 1024;  // (row, dl) pairs per batch
+
+template <int CPL, bool VEC, bool BF16, bool WBF16>
+__global__ void __launch_bounds__(kDxThreads)
+    dx_slots_kernel(const void* __restrict__ Wv, const int32_t* __restrict__ idx,
+                    const float* __restrict__ slot, const void* addv, void* dxv, int T, int d, int N_r, int k, int tokens_per_cta) {
+  constexpr int CW = 32 * CPL;
+  extern __shared__ __align__(16) float sm[];
+  float* Ws = sm;                                            // [N_r + 1][CW]
+  int2* pairs = reinterpret_cast<int2*>(sm + (N_r + 1) * CW);  // [kDxPairs]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kDxThreads / 32;
+  const int c0 = blockIdx.x * CW;
+  const long t_begin = (long)blockIdx.y * tokens_per_cta;
+  const long t_end = t_begin + tokens_per_cta < T ? t_begin + tokens_per_cta : T;
+  for (int i = threadIdx.x; i < (N_r + 1) * CW; i += kDxThreads) {
+    const int e = i / CW, c = c0 + i % CW;
+    float v = 0.0f;
+    if (e < N_r && c < d) {
+      if constexpr (WBF16) v = mr_bf16_to_f32(static_cast<const uint16_t*>(Wv)[(long)e * d + c]);
+      else v = static_cast<const float*>(Wv)[(long)e * d + c];
+    }
+    Ws[i] = v;
+  }
+  // columns of this lane: CPL consecutive ones (VEC) or every 32nd
+  auto col = [&](int i) { return VEC ? lane * CPL + i : lane + 32 * i; };
+  const int batch = kDxPairs / k;
+  for (long tb = t_begin; tb < t_end; tb += batch) {
+    const int nt = (int)(t_end - tb < batch ? t_end - tb : batch);
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * k; i += kDxThreads) {
+      const int e = idx[tb * k + i];
+      const bool ok = e >= 0 && e < N_r;
+      pairs[i] = make_int2((ok ? e : N_r) * CW, ok ? __float_as_int(slot[tb * k + i]) : 0);
+    }
+    __syncthreads();
+    for (int q = warp; q < nt; q += kWarps) {
+      float acc[CPL];
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[i] = 0.0f;
+      const int2* p = pairs + q * k;
+#pragma unroll 4
+      for (int j = 0; j < k; ++j) {
+        const int2 pr = p[j];
+        const float a = __int_as_float(pr.y);
+        const float* wr = Ws + pr.x;
+        if constexpr (VEC && CPL == 4) {
+          const float4 wv = *reinterpret_cast<const float4*>(wr + lane * 4);
+          acc[0] = fmaf(a, wv.x, acc[0]);
+          acc[1] = fmaf(a, wv.y, acc[1]);
+          acc[2] = fmaf(a, wv.z, acc[2]);
+          acc[3] = fmaf(a, wv.w, acc[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) acc[i] = fmaf(a, wr[col(i)], acc[i]);
+        }
+      }
+      const long base = (tb + q) * d + c0;
+      if constexpr (VEC) {
+        if (c0 + lane * CPL < d) {  // d is a multiple of CPL
+          if constexpr (BF16) {
+            uint32_t o[CPL / 2];
+            if (addv) {
+              const uint32_t* a =
+                  reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(addv) + base) +
+                  lane * (CPL / 2);
+#pragma unroll
+              for (int i = 0; i < CPL / 2; ++i) {
+                float lo, hi;
+                bf16x2_unpack(a[i], lo, hi);
+                acc[2 * i] += lo;
+                acc[2 * i + 1] += hi;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < CPL / 2; ++i) o[i] = bf16x2_pack_rn(acc[2 * i], acc[2 * i + 1]);
+            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(dxv) + base) +
+                            lane * (CPL / 2);
+            if constexpr (CPL == 4) __stcs(reinterpret_cast<uint2*>(out), make_uint2(o[0], o[1]));
+            else __stcs(out, o[0]);
+          } else {
+            const float* a = addv ? static_cast<const float*>(addv) + base + lane * CPL : nullptr;
+            float* out = static_cast<float*>(dxv) + base + lane * CPL;
+            if (a) {
+#pragma unroll
+              for (int i = 0; i < CPL; ++i) acc[i] += a[i];
+            }
+            if constexpr (CPL == 4)
+              __stcs(reinterpret_cast<float4*>(out), make_float4(acc[0], acc[1], acc[2], acc[3]));
+            else
+              __stcs(reinterpret_cast<float2*>(out), make_float2(acc[0], acc[1]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+          const int c = col(i);
+          if (c0 + c >= d) continue;
+          if constexpr (BF16) {
+            if (addv) acc[i] += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[base + c]);
+            const __nv_bfloat16 b = __float2bfloat16_rn(acc[i]);
+            static_cast<uint16_t*>(dxv)[base + c] = *reinterpret_cast<const uint16_t*>(&b);
+          } else {
+            if (addv) acc[i] += static_cast<const float*>(addv)[base + c];
+            static_cast<float*>(dxv)[base + c] = acc[i];
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---- sigmoid: dW[e] = sum over the sorted rows r of e of dl[perm[r]] * x[perm[r]/k]
+//
+// Each expert's segment is cut into pieces of kDwRows sorted rows; a CTA takes
+// one piece and one slab of columns (consecutive CTAs share the slab, so its
+// columns of x stay in L2 while every expert reads them).  An expert's first
+// piece goes to dW, the others to `part`, and dw_join_kernel adds them in
+// order: no atomics, a long segment is spread over many SMs.
+constexpr int kDwRows = 256;
+constexpr int kDwThreads = 128;
+
+// Extra pieces (beyond an expert's first) of all experts before expert e are
+// numbered consecutively; there are at most T*k / kDwRows of them.
+struct Piece {
+  int e, row0, rows, extra;  // extra: index in `part`, -1 for an expert's first piece
+};
+
+// Finds piece `b` (all threads of the CTA call it; e = -1 past the last one).
+__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets, int N_r, int n,
+                                            int b) {
+  __shared__ Piece found;
+  __shared__ int wsum[2][kDwThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = (N_r + kDwThreads - 1) / kDwThreads;
+  const int e0 = tid * c, e1 = e0 + c < N_r ? e0 + c : N_r;
+  auto rows_of = [&](int e, int& lo) {
+    lo = offsets[e];
+    int hi = offsets[e + 1];
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > n ? n : hi;
+    return hi > lo ? hi - lo : 0;
+  };
+  int mine = 0, extra = 0;
+  for (int e = e0; e < e1; ++e) {
+    int lo;
+    const int p = (rows_of(e, lo) + kDwRows - 1) / kDwRows;
+    mine += p;
+    extra += p > 1 ? p - 1 : 0;
+  }
+  int a = mine, x = extra;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int ya = __shfl_up_sync(0xffffffffu, a, off), yx = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) {
+      a += ya;
+      x += yx;
+    }
+  }
+  if (lane == 31) {
+    wsum[0][warp] = a;
+    wsum[1][warp] = x;
+  }
+  if (tid == 0) found.e = -1;
+  __syncthreads();
+  int before = a - mine, xb = x - extra;
+  for (int w = 0; w < warp; ++w) {
+    before += wsum[0][w];
+    xb += wsum[1][w];
+  }
+  if (b >= before && b < before + mine) {
+    for (int e = e0; e < e1; ++e) {
+      int lo;
+      const int cnt = rows_of(e, lo), p = (cnt + kDwRows - 1) / kDwRows;
+      if (b < before + p) {
+        const int i = b - before;
+        found.e = e;
+        found.row0 = lo + i * kDwRows;
+        found.rows = cnt - i * kDwRows < kDwRows ? cnt - i * kDwRows : kDwRows;
+        found.extra = i == 0 ? -1 : xb + i - 1;
+        break;
+      }
+      before += p;
+      xb += p > 1 ? p - 1 : 0;
+    }
+  }
+  __syncthreads();
+  return found;
+}
+
+// V: uint4 (8 bf16 or 4 fp32 columns per thread) or one element.
+template <typename V, bool BF16>
+__global__ void __launch_bounds__(kDwThreads)
+    dw_slots_kernel(const V* __restrict__ x, const int32_t* __restrict__ perm,
+                    const int32_t* __restrict__ offsets, const float* __restrict__ slot, int n,
+                    int N_r, int k, long nvec, float* __restrict__ dW, float* __restrict__ part) {
+  using R = RowVec<V, BF16>;
+  constexpr int NE = R::kElems;
+  constexpr int U = 8;
+  const Piece pc = find_piece(offsets, N_r, n, blockIdx.x);
+  if (pc.e < 0) return;
+  __shared__ int tok[kDwRows];
+  __shared__ float gs[kDwRows];
+  for (int i = threadIdx.x; i < pc.rows; i += kDwThreads) {
+    const int p = perm[pc.row0 + i];
+    const bool ok = p >= 0 && p < n;
+    if (!ok) mr_raise(MR_FLAG_BAD_INDEX);
+    tok[i] = ok ? p / k : -1;
+    gs[i] = ok ? slot[p] : 0.0f;
+  }
+  __syncthreads();
+  const long v = (long)blockIdx.y * kDwThreads + threadIdx.x;
+  if (v >= nvec) return;
+  float acc[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+  for (int r = 0; r < pc.rows; r += U) {
+    V xv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = r + u < pc.rows ? tok[r + u] : -1;
+      xv[u] = t >= 0 ? ld_stream(x + (long)t * nvec + v) : V{};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float g = r + u < pc.rows ? gs[r + u] : 0.0f;
+      float xf[NE];
+      R::unpack(xv[u], xf);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[i] = fmaf(g, xf[i], acc[i]);
+    }
+  }
+  const long d = nvec * NE;
+  float* out = (pc.extra < 0 ? dW + (long)pc.e * d : part + (long)pc.extra * d) + v * NE;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) out[i] = acc[i];
+}
+
+// dW[e] += the extra pieces of e, in order; 0 for an expert without rows.
+__global__ void __launch_bounds__(256)
+    dw_join_kernel(const int32_t* __restrict__ offsets, int n, int N_r, int d,
+                   const float* __restrict__ part, float* __restrict__ dW) {
+  const int e = blockIdx.x;
+  __shared__ int first_s, count_s;
+  if (threadIdx.x < 32) {
+    int x = 0, mine = 0;
+    for (int i = threadIdx.x; i <= e; i += 32) {
+      int lo = offsets[i], hi = offsets[i + 1];
+      lo = lo < 0 ? 0 : lo;
+      hi = hi > n ? n : hi;
+      const int p = hi > lo ? (hi - lo + kDwRows - 1) / kDwRows : 0;
+      if (i == e) mine = p;
+      else x += p > 1 ? p - 1 : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, off);
+      mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    }
+    if (threadIdx.x == 0) {
+      first_s = x;
+      count_s = mine;
+    }
+  }
+  __syncthreads();
+  const int first = first_s, count = count_s;
+  if (count == 1) return;
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < d; c += gridDim.y * blockDim.x) {
+    float s = count ? dW[(long)e * d + c] : 0.0f;
+    for (int i = 0; i + 1 < count; ++i) s += part[(long)(first + i) * d + c];
+    dW[(long)e * d + c] = s;
+  }
+}
+
+// ---- softmax: dense fp32 products on the CUDA cores -----------------------------
+//
+// C [M, N] = A . B, fp32 fused multiply-adds: 128 x 128 tiles, K in steps of
+// 16, 256 threads of 8 x 8 elements each.  TA: A is stored [K, M] (dL for dW),
+// else [M, K] (dL for dx).  B [K, N] row-major, fp32 or bf16.  K may be split
+// over gridDim.z; slice z of C then goes to C + z * M * N (fp32) and
+// sum_slices_kernel adds them in order.
+constexpr int kGemmT = 128, kGemmK = 16;
+
+template <bool TA, bool BBF16, bool OBF16>
+__global__ void __launch_bounds__(256)
+    dense_kernel(const float* __restrict__ A, const void* __restrict__ Bv,
+                 const void* addv, void* Cv, int M, int N, int K) {
+  __shared__ float As[kGemmK][kGemmT + 4];
+  __shared__ float Bs[kGemmK][kGemmT + 4];
+  const int tid = threadIdx.x;
+  const long m0 = (long)blockIdx.y * kGemmT, n0 = (long)blockIdx.x * kGemmT;
+  const int steps = (K + kGemmK - 1) / kGemmK;
+  const int s_begin = (int)((long)steps * blockIdx.z / gridDim.z);
+  const int s_end = (int)((long)steps * (blockIdx.z + 1) / gridDim.z);
+  const int tm = tid / 16, tn = tid % 16;
+  float acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  float ra[8], rb[8];
+  auto fetch = [&](int step) {
+    const long k0 = (long)step * kGemmK;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = tid + 256 * i;
+      const int kk = TA ? q / kGemmT : q % kGemmK, mm = TA ? q % kGemmT : q / kGemmK;
+      const long kg = k0 + kk, mg = m0 + mm;
+      ra[i] = kg < K && mg < M ? A[TA ? kg * M + mg : mg * K + kg] : 0.0f;
+      const long kb = k0 + q / kGemmT, ng = n0 + q % kGemmT;
+      rb[i] = 0.0f;
+      if (kb < K && ng < N) {
+        if constexpr (BBF16) rb[i] = mr_bf16_to_f32(static_cast<const uint16_t*>(Bv)[kb * N + ng]);
+        else rb[i] = static_cast<const float*>(Bv)[kb * N + ng];
+      }
+    }
+  };
+  if (s_begin < s_end) fetch(s_begin);
+  for (int s = s_begin; s < s_end; ++s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = tid + 256 * i;
+      if constexpr (TA) As[q / kGemmT][q % kGemmT] = ra[i];
+      else As[q % kGemmK][q / kGemmK] = ra[i];
+      Bs[q / kGemmT][q % kGemmT] = rb[i];
+    }
+    __syncthreads();
+    if (s + 1 < s_end) fetch(s + 1);
+#pragma unroll
+    for (int kk = 0; kk < kGemmK; ++kk) {
+      float a[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<float4*>(a + i) =
+            *reinterpret_cast<const float4*>(&As[kk][tm * 4 + (i / 4) * 64]);
+        *reinterpret_cast<float4*>(b + i) =
+            *reinterpret_cast<const float4*>(&Bs[kk][tn * 4 + (i / 4) * 64]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long m = m0 + tm * 4 + (i / 4) * 64 + i % 4;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const long c = n0 + tn * 4 + (j / 4) * 64 + j % 4;
+      if (c >= N) continue;
+      float v = acc[i][j];
+      const long o = m * N + c;
+      if constexpr (OBF16) {
+        if (addv) v += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[o]);
+        const __nv_bfloat16 b = __float2bfloat16_rn(v);
+        static_cast<uint16_t*>(Cv)[o] = *reinterpret_cast<const uint16_t*>(&b);
+      } else {
+        if (addv) v += static_cast<const float*>(addv)[o];
+        static_cast<float*>(Cv)[(long)blockIdx.z * M * N + o] = v;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256)
+    sum_slices_kernel(const float* __restrict__ part, int slices, long n, float* __restrict__ out) {
+  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (long)gridDim.x * blockDim.x) {
+    float s = 0.0f;
+    for (int z = 0; z < slices; ++z) s += part[z * n + i];
+    out[i] = s;
+  }
+}
+
+}  // namespace rb
+}  // namespace mr

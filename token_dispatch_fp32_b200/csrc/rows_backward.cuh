@@ -1,0 +1,208 @@
+// rows_backward.cuh -- gradients of the row movers (gather.cuh, combine.cuh).
+//
+// combine, forward: y[t] = sum_j w[t,j] * E[r] + shared[t], r = inv[t*k + j]
+// (Kimi K2 "Add shared output" page: new_x[idxs] = outs, weighted sum over k,
+// y + shared).  The two roundings of y pass a gradient through unchanged:
+//   dE[r]   = w[t,j] * dy[t]          (rounded once to the row dtype)
+//   dw[t,j] = sum_c dy[t,c] * E[r,c]  (fp32)
+//   dshared = dy.
+// gather, forward: xs[r] = x[t] for the k rows r of token t, hence
+//   dx[t] = sum_j dxs[inv[t*k + j]] (+ add[t])   (fp32, rounded once).
+//
+// Both are bound by HBM (at most 3 flops per element moved): combine_backward
+// reads dy once and each expert row once and writes each expert row's gradient
+// once.  One CTA per token, so dy stays in registers for the k rows and the k
+// dot products meet inside the CTA in a fixed order: no atomics, the result
+// does not change from run to run.
+#pragma once
+
+#include "combine.cuh"
+#include "rows_common.cuh"
+
+namespace mr {
+
+// A vector of a row as fp32 values: bf16 pairs per word (BF16) or one fp32
+// per word.
+template <typename V, bool BF16>
+struct RowVec {
+  static constexpr int kWords = (int)(sizeof(V) / 4);
+  static constexpr int kElems = BF16 ? 2 * kWords : kWords;
+  static __device__ __forceinline__ void unpack(const V& v, float (&f)[kElems]) {
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) {
+      if constexpr (BF16) bf16x2_unpack(word(v, q), f[2 * q], f[2 * q + 1]);
+      else f[q] = __uint_as_float(word(v, q));
+    }
+  }
+  static __device__ __forceinline__ V pack(const float (&f)[kElems]) {
+    V v;
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) {
+      if constexpr (BF16) set_word(v, q, bf16x2_pack_rn(f[2 * q], f[2 * q + 1]));
+      else set_word(v, q, __float_as_uint(f[q]));
+    }
+    return v;
+  }
+};
+// One element per step, for rows that no vector width fits.
+template <>
+struct RowVec<uint16_t, true> {
+  static constexpr int kElems = 1;
+  static __device__ __forceinline__ void unpack(const uint16_t& v, float (&f)[1]) {
+    f[0] = mr_bf16_to_f32(v);
+  }
+  static __device__ __forceinline__ uint16_t pack(const float (&f)[1]) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(f[0]);
+    return *reinterpret_cast<const uint16_t*>(&b);
+  }
+};
+template <>
+struct RowVec<float, false> {
+  static constexpr int kElems = 1;
+  static __device__ __forceinline__ void unpack(const float& v, float (&f)[1]) { f[0] = v; }
+  static __device__ __forceinline__ float pack(const float (&f)[1]) { return f[0]; }
+};
+
+// A load of memory that this kernel may also write (add may be dx): not
+// through the read-only path.
+template <typename V>
+__device__ __forceinline__ V ld_plain(const V* p) {
+  return *reinterpret_cast<const volatile V*>(p);
+}
+template <>
+__device__ __forceinline__ uint4 ld_plain<uint4>(const uint4* p) {
+  return __ldcs(p);
+}
+template <>
+__device__ __forceinline__ Vec32 ld_plain<Vec32>(const Vec32* p) {
+  Vec32 r;
+  asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                 "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p));
+  return r;
+}
+
+constexpr int kBwdGroup = 8;  // slots whose rows are in flight at once
+
+// E may be null (no dw wanted), dE may be null (frozen experts).
+template <typename V, bool BF16>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_backward_kernel(const V* __restrict__ dy, const V* __restrict__ E,
+                            const float* __restrict__ w, const int32_t* __restrict__ inv,
+                            V* __restrict__ dE, float* __restrict__ dw, long nvec, int k) {
+  using R = RowVec<V, BF16>;
+  constexpr int NE = R::kElems;
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ long row_s[kRowMaxK];
+  __shared__ float w_s[kRowMaxK];
+  __shared__ float red[kWarps][kBwdGroup];
+  const long t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < k) {
+    row_s[threadIdx.x] = inv[t * k + threadIdx.x];
+    w_s[threadIdx.x] = w[t * k + threadIdx.x];
+  }
+  __syncthreads();
+  const V* g = dy + t * nvec;
+  for (int j0 = 0; j0 < k; j0 += kBwdGroup) {
+    long row[kBwdGroup];
+    float dot[kBwdGroup];
+#pragma unroll
+    for (int u = 0; u < kBwdGroup; ++u) {
+      row[u] = j0 + u < k ? row_s[j0 + u] : -1;
+      dot[u] = 0.0f;
+    }
+    for (long v = threadIdx.x; v < nvec; v += kRowThreads) {
+      const V gv = ld_stream(g + v);
+      V e[kBwdGroup];
+      if (E) {
+#pragma unroll
+        for (int u = 0; u < kBwdGroup; ++u)
+          e[u] = row[u] >= 0 ? ld_stream(E + row[u] * nvec + v) : V{};
+      }
+      float gf[NE];
+      R::unpack(gv, gf);
+#pragma unroll
+      for (int u = 0; u < kBwdGroup; ++u) {
+        if (row[u] < 0) continue;
+        if (E) {
+          float ef[NE];
+          R::unpack(e[u], ef);
+#pragma unroll
+          for (int i = 0; i < NE; ++i) dot[u] = fmaf(gf[i], ef[i], dot[u]);
+        }
+        if (dE) {
+          const float wj = w_s[j0 + u];
+          float o[NE];
+#pragma unroll
+          for (int i = 0; i < NE; ++i) o[i] = wj * gf[i];
+          st_stream(dE + row[u] * nvec + v, R::pack(o));
+        }
+      }
+    }
+    if (dw) {
+#pragma unroll
+      for (int u = 0; u < kBwdGroup; ++u) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+          dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], off);
+        if (lane == 0) red[warp][u] = dot[u];
+      }
+      __syncthreads();
+      if (threadIdx.x < kBwdGroup && j0 + threadIdx.x < k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) s += red[q][threadIdx.x];
+        dw[t * k + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <typename V, bool BF16>
+__global__ void __launch_bounds__(kRowThreads)
+    gather_backward_kernel(const V* __restrict__ dxs, const int32_t* __restrict__ inv,
+                           const V* add, V* dx, long T, long nvec,
+                           int k) {
+  using R = RowVec<V, BF16>;
+  constexpr int NE = R::kElems;
+  __shared__ long row_s[kRowMaxK];
+  for (long t = blockIdx.x; t < T; t += gridDim.x) {
+    if (threadIdx.x < k) row_s[threadIdx.x] = inv[t * k + threadIdx.x];
+    __syncthreads();
+    for (long v = threadIdx.x; v < nvec; v += kRowThreads) {
+      V av{};
+      if (add) av = ld_plain(add + t * nvec + v);
+      float acc[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+      for (int j0 = 0; j0 < k; j0 += kBwdGroup) {
+        V e[kBwdGroup];
+#pragma unroll
+        for (int u = 0; u < kBwdGroup; ++u) {
+          const long r = j0 + u < k ? row_s[j0 + u] : -1;
+          e[u] = r >= 0 ? ld_stream(dxs + r * nvec + v) : V{};
+        }
+#pragma unroll
+        for (int u = 0; u < kBwdGroup; ++u) {  // V{} of a missing slot adds 0
+          float ef[NE];
+          R::unpack(e[u], ef);
+#pragma unroll
+          for (int i = 0; i < NE; ++i) acc[i] += ef[i];
+        }
+      }
+      if (add) {
+        float af[NE];
+        R::unpack(av, af);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) acc[i] += af[i];
+      }
+      st_stream(dx + t * nvec + v, R::pack(acc));
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace mr
