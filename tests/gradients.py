@@ -118,11 +118,12 @@ def check(got, want, bound, dtype="f32", name=""):
 
 
 def expert_w4(x, perm, offsets, q, scales, group, k):
-    """(out by sorted row, sum of |scale * q * x| behind each) in binary64."""
+    """(out by sorted row, sum of |scale * q * x| behind each, sum of |scale *
+    x|) in binary64."""
     N, n_out, half = q.shape
     d = 2 * half
     rows = len(perm)
-    out, mag = np.zeros((rows, n_out)), np.zeros((rows, n_out))
+    out, mag, magx = (np.zeros((rows, n_out)) for _ in range(3))
     for e in range(N):
         a, b = offsets[e], offsets[e + 1]
         if a == b:
@@ -130,8 +131,10 @@ def expert_w4(x, perm, offsets, q, scales, group, k):
         v = np.empty((n_out, d))
         v[:, 0::2] = (q[e] & 15).astype(np.float64) - 8
         v[:, 1::2] = (q[e] >> 4).astype(np.float64) - 8
-        v *= np.repeat(scales[e].astype(np.float64), group, axis=1)[:, :d]
+        sc = np.repeat(scales[e].astype(np.float64), group, axis=1)[:, :d]
+        v *= sc
         xe = x[perm[a:b] // k]
         out[a:b] = xe @ v.T
         mag[a:b] = np.abs(xe) @ np.abs(v).T
-    return out, mag
+        magx[a:b] = np.abs(xe) @ np.abs(sc).T
+    return out, mag, magx

@@ -1,10 +1,12 @@
 """The expert layer on 4-bit weights (mr_expert_gemv_gather_w4) on the GPU
 against binary64 (tests/gradients.py: expert_w4).
 
-Bound: a bf16 x times a 4-bit integer is exact in fp32, a group's products are
-added by MMA steps of 16 (each rounds within 2 fp32 steps of its largest
-partial sum), groups and warps in fp32: at most (d / 16 + 16) * 2^-23 of the
-sum of the magnitudes, plus half a step of the bf16 output."""
+Bound: 32 columns at a time, the kernel forms -24 sum x and adds sum (16 + u) x
+to it, u the nibble: four MMA steps, each exact in its products and rounding
+within 2 fp32 steps (2 * 2^-23) of its largest partial sum, which is at most
+(24 + 31) sum |x|; hence 4 * 2 * 55 = 440 * 2^-23 of the scaled sum of |x|.
+Groups and warps then add in fp32: at most (d / 128 + 16) * 2^-23 of the sum
+of the magnitudes.  Plus half a step of the bf16 output."""
 import numpy as np
 import pytest
 import torch
@@ -29,8 +31,8 @@ def _problem(T, k, N_r, n_out, d, group, sdt, seed, hot=0):
     return x, perm, offsets, inv, q, s
 
 
-def _bound(d, mag):
-    return (d / 16 + 16) * 2.0 ** -23 * mag
+def _bound(d, mag, magx):
+    return ((d / 128 + 16) * mag + 440 * magx) * 2.0 ** -23
 
 
 CASES = [  # T, k, N_r, n_out, d, group, scales, hot
@@ -54,8 +56,8 @@ def test_expert_w4(T, k, N_r, n_out, d, group, sdt, hot):
     out = mr.mr_expert_gemv_gather_w4(_dev(x), k, _i32(perm), _i32(offsets), W4, N_r, n_out,
                                       group, scale_dtype=st)
     assert mr.mr_get_error() == mr.MR_OK
-    want, mag = gr.expert_w4(widen(x), perm, offsets, q, widen(s), group, k)
-    gr.check(widen(_host(out)), want, _bound(d, mag), "bf16", "out")
+    want, mag, magx = gr.expert_w4(widen(x), perm, offsets, q, widen(s), group, k)
+    gr.check(widen(_host(out)), want, _bound(d, mag, magx), "bf16", "out")
     # rows already sorted (perm None), and a second run: bit for bit the same
     xs = _dev(np.ascontiguousarray(x[perm // k]))
     again = mr.mr_expert_gemv_gather_w4(xs, k, None, _i32(offsets), W4, N_r, n_out, group,
@@ -74,7 +76,7 @@ def test_expert_w4_exact_on_integers(group):
     q = rng.integers(0, 256, (N_r, n_out, d // 2)).astype(np.uint8)
     s = (2.0 ** rng.integers(-3, 3, (N_r, n_out, d // group))).astype(np.float32)
     xb = torch.from_numpy(x).bfloat16().cuda()
-    want, _ = gr.expert_w4(x.astype(np.float64), perm, offsets, q, s, group, k)
+    want, _, _ = gr.expert_w4(x.astype(np.float64), perm, offsets, q, s, group, k)
     for st in (torch.bfloat16, torch.float32):
         W4 = mr.mr_expert_pack_w4(torch.from_numpy(q).cuda(), _f32(s).to(st), group)
         out = mr.mr_expert_gemv_gather_w4(xb, k, _i32(perm), _i32(offsets), W4, N_r, n_out, group,
@@ -99,8 +101,8 @@ def test_expert_w4_leaves_other_rows():
     p, o = perm.cpu().numpy(), offsets.cpu().numpy()
     n = o[-1]
     assert n == T * k - 2
-    want, mag = gr.expert_w4(widen(x), p[:n], o, q, widen(s), 32, k)
-    gr.check(widen(_host(out))[:n], want, _bound(d, mag), "bf16", "out")
+    want, mag, magx = gr.expert_w4(widen(x), p[:n], o, q, widen(s), 32, k)
+    gr.check(widen(_host(out))[:n], want, _bound(d, mag, magx), "bf16", "out")
     assert (out[n:] == 7.0).all()
 
 
@@ -157,9 +159,9 @@ def test_decode_step_of_a_moe_layer(mode):
     torch.cuda.synchronize()
     assert mr.mr_get_error() == mr.MR_OK
     idx, w, E, offsets, perm, inv, y = got
-    want, mag = gr.expert_w4(widen(x), perm.cpu().numpy(), offsets.cpu().numpy(), q, widen(s),
+    want, mag, magx = gr.expert_w4(widen(x), perm.cpu().numpy(), offsets.cpu().numpy(), q, widen(s),
                              group, k)
-    gr.check(widen(_host(E)), want, _bound(d, mag), "bf16", "experts")
+    gr.check(widen(_host(E)), want, _bound(d, mag, magx), "bf16", "experts")
     terms = w.double()[:, :, None] * E.double()[inv.long()].reshape(T, k, -1)
     ry, mag = terms.sum(1).cpu().numpy(), terms.abs().sum(1).cpu().numpy()
     gr.check(widen(_host(y)), ry, (k + 1) * gr.U * mag, "bf16", "y")

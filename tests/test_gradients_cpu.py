@@ -168,8 +168,8 @@ def test_expert_w4_refusals():
     assert size(4, 64, 256, 32, 7) == 0
     n = size(4, 64, 256, 32, 1)
     assert n == 4 * 64 * 256 // 2 + 4 * 64 * 8 * 2
-    # padded to 16 rows and 128 columns
-    assert size(1, 1, 8, 128, 0) == 1024 + 16 * 4
+    # padded to 64 rows and 128 columns
+    assert size(1, 1, 8, 128, 0) == 4096 + 64 * 4
     pack = L.mr_expert_pack_w4  # q, scales, sdt, N, n_out, d, group, packed, bytes, stream
     assert pack(P, P, 1, 4, 64, 256, 32, P, n - 1, None) == mr.MR_ERR_INVALID_ARG
     assert pack(P, P, 1, 4, 64, 252, 32, P, n, None) == mr.MR_ERR_UNSUPPORTED

@@ -7,78 +7,97 @@
 // for the sorted row j of expert e, groups G of 32, 64 or 128 columns.  A few
 // rows per expert make this a stream of the hit experts' weights from HBM
 // (n_out * d / 2 bytes each plus the scales): the kernel's work per weight has
-// to stay below what the SMs issue while those bytes arrive, about three
-// instructions per weight.  So a weight is widened once, two at a time, by an
-// integer trick (nibble u in the low mantissa bits of 128.0 is 128 + u in
-// bf16; subtracting 136 is exact), and multiplied by tensor-core MMAs with the
-// weights as the 16-row operand and up to 8 rows of x as the 8 columns
-// (mma.sync m16n8k16: at this shape the tensor pipe is nearly idle; a 128-row
-// tcgen05 tile would first have to pass the widened weights, four times the
-// bytes, through shared or tensor memory).  Products of bf16 x by integers in
-// [-8, 7] are exact in fp32; each group's fp32 sum is scaled and added in
-// fp32, so the only rounding to fewer bits is the output's.
+// to stay below what the SMs issue while those bytes arrive: about 50 cycles
+// of an SM for 16 x 128 weights.  So
+//  * weights meet x in tensor-core MMAs with the weights as the 16-row operand
+//    and 8 rows of x as the columns (mma.sync m16n8k16: at this shape the
+//    tensor pipe is nearly idle, and its operands come from registers; a
+//    128-row tcgen05 tile would first have to pass the widened weights, four
+//    times the bytes, through shared or tensor memory);
+//  * a nibble u becomes the bf16 value 16 + u by one AND-OR of two weights (its
+//    four bits are the upper mantissa bits of 16.0), rotated into place by one
+//    shift; nothing is subtracted per weight: the sums start from -24 * sum x
+//    of the group's columns, which one more MMA pair with a constant operand
+//    forms for all rows at once.
+// Every product is exact in fp32.  A group's sum runs through at most 55 * sum
+// |x| (24 + 31) where |q - 8| alone would reach 8 * sum |x|, in fp32; it is
+// then scaled and added in fp32, and the result rounded to bf16 once.
 //
-// Packed layout (written once by w4_pack_kernel): the weights are cut into
-// blocks of 16 output rows x 128 columns, block (e, mt, kb) at index
-// (e * MT + mt) * KB + kb, 1024 bytes: 512 for rows 0-7 and 512 for rows 8-15
-// of the block, lane l's 16 bytes at 16 * l.  They are four words, word i for
-// the columns 32 i + 8 (l % 4) .. + 7 of row l / 4 (+ 8): the columns the lane
-// feeds to two MMA steps, so that a warp's load is 512 contiguous bytes, the
-// lane's share of x is 16 contiguous bytes, and one MMA never spans two
-// groups.  In a word, column 2 p of the eight is the nibble at bit 4 p, column
-// 2 p + 1 the one at bit 16 + 4 p.  Scales follow as [block][16 rows][128 /
-// group] in their own type.  Padded rows and columns hold the value 0 (nibble
-// 8) and scale 0.
+// Packed layout (written once by w4_pack_kernel): units of 64 output rows x 128
+// columns, unit (e, tile, kb) at index (e * tiles + tile) * KB + kb.  A unit is
+// read in four steps i of 32 columns.  With lane l of a warp standing for the
+// rows 16 m + l / 4 and 16 m + 8 + l / 4 (m = 0..3) and the columns 32 i + 8 (l
+// % 4) .. + 7 -- what it feeds to two steps of an m16n8k16 MMA, so that the
+// lane's share of x is 16 contiguous bytes -- its weights of step i are four
+// words (m = 0..3) for the first rows at 1024 i + 16 l and four for the second
+// at 1024 i + 512 + 16 l.  In a word, column 2 p of the eight is the nibble at
+// bit 3 + 4 p, column 2 p + 1 the one at bit 19 + 4 p (modulo 32).  The unit's scales follow
+// in their own type as [128 / group][8 rows l / 4][4 m][2], so that a lane
+// reads its eight scales of a step at once.  Padded rows and columns hold the
+// value 0 (nibble 8) and scale 0.
+//
+// The kernel is persistent, two CTAs per SM.  An item is 64 output rows of one
+// expert against up to `xr` of its sorted rows; the CTA's eight warps split
+// the columns (warp w takes units w, w + 8, ..) and meet in shared memory at
+// the item's end, adding in warp order.  Each warp has its own ring of units
+// in shared memory, filled by one bulk copy each, and requests a unit as soon
+// as it has finished the one whose place it takes, through the ends of items,
+// so that the stream from HBM does not pause; no warp waits for another but at
+// an item's end.  x comes through L1.  Every mbarrier wait is bounded.
 #pragma once
 
+#include <type_traits>
+
+#include "expert_gemm.cuh"
 #include "mr_common.cuh"
 
 namespace mr {
 namespace w4 {
 
-constexpr int kRows = 16;      // output rows per block (MMA M)
-constexpr int kCols = 128;     // columns per block
-constexpr int kBlockBytes = 1024;
+using namespace mr::tc;
+
+constexpr int kTile = 64;      // output rows per unit and item
+constexpr int kCols = 128;     // columns per unit
+constexpr int kWeightBytes = kTile * kCols / 2;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMT = 2;         // row blocks per CTA
+constexpr int kMaxExperts = 1024;
+constexpr int kStages = 2;     // units per warp's ring
+constexpr int kRowsPerPass = 16;  // sorted rows per item (two column tiles of the MMA)
 
 struct Layout {
-  int MT, KB;            // blocks along n_out and d
-  long blocks;           // N_r * MT * KB
-  size_t scale_off;      // bytes of the weight part
+  int tiles, KB;         // tiles of n_out, units along d
+  int unit_bytes;
   size_t total;
 };
 
 inline Layout make_layout(int N_r, int n_out, int d, int group, int scale_bytes) {
   Layout l;
-  l.MT = (n_out + kRows - 1) / kRows;
+  l.tiles = (n_out + kTile - 1) / kTile;
   l.KB = (d + kCols - 1) / kCols;
-  l.blocks = (long)N_r * l.MT * l.KB;
-  l.scale_off = (size_t)l.blocks * kBlockBytes;
-  l.total = l.scale_off + (size_t)l.blocks * kRows * (kCols / group) * scale_bytes;
+  l.unit_bytes = kWeightBytes + kTile * (kCols / group) * scale_bytes;
+  l.total = (size_t)N_r * l.tiles * l.KB * l.unit_bytes;
   return l;
 }
 
 // q [N_r, n_out, d / 2] (column 2 i in the low nibble of byte i), scales
-// [N_r, n_out, ceil(d / group)] -> the packed layout.  One warp per block.
+// [N_r, n_out, ceil(d / group)] -> the packed layout.  One CTA per unit.
 template <typename S>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
     w4_pack_kernel(const uint8_t* __restrict__ q, const S* __restrict__ scales, int n_out, int d,
-                   int group, int MT, int KB, long blocks, uint4* __restrict__ wp,
-                   S* __restrict__ sp) {
-  const int lane = threadIdx.x & 31;
-  const long b = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (b >= blocks) return;
+                   int group, int tiles, int KB, int unit_bytes, uint8_t* __restrict__ packed) {
+  const int lane = threadIdx.x & 31, i = threadIdx.x >> 5;
+  const long b = blockIdx.x;
   const int kb = (int)(b % KB);
-  const int mt = (int)((b / KB) % MT);
-  const long e = b / ((long)KB * MT);
+  const int tile = (int)((b / KB) % tiles);
+  const long e = b / ((long)KB * tiles);
+  uint8_t* unit = packed + b * unit_bytes;
+  const int c0 = kb * kCols + 32 * i + 8 * (lane % 4);
   for (int h = 0; h < 2; ++h) {
-    const int n = mt * kRows + 8 * h + lane / 4;
     uint32_t w[4];
-    for (int i = 0; i < 4; ++i) {
-      const int c0 = kb * kCols + 32 * i + 8 * (lane % 4);
-      uint32_t v = 0x88888888u;  // d % 8 == 0: the eight columns are all in or all out
+    for (int m = 0; m < 4; ++m) {
+      const int n = tile * kTile + m * 16 + 8 * h + lane / 4;
+      uint32_t v = 0x44444444u;  // nibbles of 8, rotated; the eight columns are all in or all out
       if (n < n_out && c0 < d) {
         const uint8_t* src = q + ((e * n_out + n) * (long)d + c0) / 2;
         v = 0;
@@ -87,237 +106,348 @@ __global__ void __launch_bounds__(256)
           v |= (byte & 15u) << (4 * p);
           v |= (byte >> 4) << (16 + 4 * p);
         }
+        v = __funnelshift_l(v, v, 3);
       }
-      w[i] = v;
+      w[m] = v;
     }
-    wp[b * (kBlockBytes / 16) + 32 * h + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(unit + 1024 * i + 512 * h + 16 * lane) =
+        make_uint4(w[0], w[1], w[2], w[3]);
   }
   const int ng = kCols / group, groups = (d + group - 1) / group;
-  for (int i = lane; i < kRows * ng; i += 32) {
-    const int n = mt * kRows + i / ng, g = kb * ng + i % ng;
+  S* sp = reinterpret_cast<S*>(unit + kWeightBytes);
+  for (int o = threadIdx.x; o < kTile * ng; o += 128) {
+    const int h = o & 1, m = (o >> 1) & 3, r = (o >> 3) & 7;
+    const int n = tile * kTile + m * 16 + 8 * h + r, g = kb * ng + (o >> 6);
     S v{};
     if (n < n_out && g < groups) v = scales[(e * n_out + n) * (long)groups + g];
-    sp[b * (kRows * ng) + i] = v;
+    sp[o] = v;
   }
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(uint16_t v) { return mr_bf16_to_f32(v); }
-
-// Nibbles at bits s and 16 + s of w as two bf16 values minus 8 (low half: the
-// nibble at bit s).
-__device__ __forceinline__ uint32_t widen2(uint32_t w, int s) {
-  const uint32_t m = ((w >> s) & 0x000f000fu) | 0x43004300u;  // 128 + u
-  const uint32_t k136 = 0x43084308u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&k136));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// 16 + u of the weight pair p of w, as two bf16 values.
+__device__ __forceinline__ uint32_t widen2(uint32_t w, int p) {
+  const uint32_t v = p ? __funnelshift_r(w, w, 4 * p) : w;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(r) : "r"(v), "r"(0x41804180u));
+  return r;
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
 }
 
 struct Params {
   const uint16_t* x;
-  const int32_t* perm;     // null: x holds the sorted rows
+  const int32_t* perm;  // null: x holds the sorted rows
   const int32_t* offsets;
-  const uint4* wp;
-  const void* sp;
+  const uint8_t* wp;
   uint16_t* out;
-  int T, d, k, N_r, n_out, MT, KB;
-  int rows_mode;  // gridDim.y counts sorted rows (a row that opens its segment works), else experts
+  int T, d, k, N_r, n_out, tiles, KB, unit_bytes, xr;
 };
 
-// One block of 128 columns of kMT row blocks against NT * 8 rows of x.
-template <int GROUP, typename S>
-struct Frag {
-  static constexpr int kNg = kCols / GROUP;
-  uint4 w[kMT][2];
-  S s[kMT][2][kNg];
-
-  __device__ __forceinline__ void load(const Params& P, long blk0, int KB, int n_mt, int lane) {
+// The scales of step i: s[2 m + h] for the row 16 m + 8 h + lane / 4.
+template <int GROUP>
+__device__ __forceinline__ void load_scales(const uint8_t* sc, int i, int lane, float (&s)[8],
+                                            uint16_t) {
+  const uint4 v = *reinterpret_cast<const uint4*>(sc + (i * 32 / GROUP) * 128 + (lane / 4) * 16);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      if (m >= n_mt) continue;
-      const long b = blk0 + (long)m * KB;
-      w[m][0] = __ldcs(P.wp + b * (kBlockBytes / 16) + lane);
-      w[m][1] = __ldcs(P.wp + b * (kBlockBytes / 16) + 32 + lane);
-      const S* sp = static_cast<const S*>(P.sp) + b * (kRows * kNg) + (lane / 4) * kNg;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (sizeof(S) * kNg == 16)
-          *reinterpret_cast<uint4*>(s[m][h]) =
-              __ldg(reinterpret_cast<const uint4*>(sp + 8 * h * kNg));
-        else if constexpr (sizeof(S) * kNg == 8)
-          *reinterpret_cast<uint2*>(s[m][h]) =
-              __ldg(reinterpret_cast<const uint2*>(sp + 8 * h * kNg));
-        else if constexpr (sizeof(S) * kNg == 4)
-          *reinterpret_cast<uint32_t*>(s[m][h]) =
-              __ldg(reinterpret_cast<const uint32_t*>(sp + 8 * h * kNg));
-        else
-          s[m][h][0] = __ldg(sp + 8 * h * kNg);
-      }
-    }
+  for (int m = 0; m < 4; ++m) {
+    s[2 * m] = __uint_as_float(w[m] << 16);
+    s[2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u);
   }
-};
-
-// A CTA owns kMT * 16 output rows of one expert; its warps split the columns
-// (warp w takes blocks w, w + 8, ..) and their partial sums meet in shared
-// memory in warp order.  NT * 8 sorted rows per pass.
-template <int GROUP, typename S, int NT>
-__device__ __forceinline__ void pass(const Params& P, int e, int mt0, int n_mt, int row0, int rows,
-                                     const int* tok, float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kNg = kCols / GROUP;
-  const uint4* xr[NT];  // this lane's row of x in each column tile (null: no row)
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = t * 8 + lane / 4;
-    const int tk = r < rows ? tok[r] : -1;
-    xr[t] = tk >= 0 ? reinterpret_cast<const uint4*>(P.x + (long)tk * P.d) + lane % 4 : nullptr;
-  }
-  float acc[kMT][NT][4];
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
-
-  const long blk0 = ((long)e * P.MT + mt0) * P.KB;
-  const int d8 = P.d / 8;
-  for (int kb = warp; kb < P.KB; kb += kWarps) {
-    Frag<GROUP, S> cur;
-    uint4 xc[NT][4];
-    cur.load(P, blk0 + kb, P.KB, n_mt, lane);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = kb * 16 + 4 * i;  // 16-byte units of x; + lane % 4 is in xr
-        xc[t][i] = xr[t] && c + lane % 4 < d8 ? __ldg(xr[t] + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      if (m >= n_mt) continue;
-#pragma unroll
-      for (int g = 0; g < kNg; ++g) {
-        float c[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[t][i] = 0.0f;
-#pragma unroll
-        for (int ii = 0; ii < GROUP / 32; ++ii) {
-          const int i = g * (GROUP / 32) + ii;
-          const uint32_t w0 = reinterpret_cast<const uint32_t*>(&cur.w[m][0])[i];
-          const uint32_t w1 = reinterpret_cast<const uint32_t*>(&cur.w[m][1])[i];
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t a[4] = {widen2(w0, 8 * s), widen2(w1, 8 * s), widen2(w0, 8 * s + 4),
-                                   widen2(w1, 8 * s + 4)};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint32_t b0 = s ? xc[t][i].z : xc[t][i].x;
-              const uint32_t b1 = s ? xc[t][i].w : xc[t][i].y;
-              mma16816(c[t], a, b0, b1);
-            }
-          }
-        }
-        const float s0 = to_f32(cur.s[m][0][g]), s1 = to_f32(cur.s[m][1][g]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          acc[m][t][0] = fmaf(s0, c[t][0], acc[m][t][0]);
-          acc[m][t][1] = fmaf(s0, c[t][1], acc[m][t][1]);
-          acc[m][t][2] = fmaf(s1, c[t][2], acc[m][t][2]);
-          acc[m][t][3] = fmaf(s1, c[t][3], acc[m][t][3]);
-        }
-      }
-    }
-  }
-  // red[warp][row of x][output row]: acc 0, 1 are columns 2 (l % 4), + 1 of
-  // output row l / 4; acc 2, 3 the same columns of output row l / 4 + 8
-  constexpr int kN = kMT * kRows;
-  float* mine = red + warp * (NT * 8 * kN);
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mine[(t * 8 + 2 * (lane % 4) + (i & 1)) * kN + m * kRows + lane / 4 + 8 * (i >> 1)] =
-            acc[m][t][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * kN; i += kThreads) {
-    const int r = i / kN, n = mt0 * kRows + i % kN;
-    if (n >= P.n_out) continue;
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w * (NT * 8 * kN) + i];
-    const __nv_bfloat16 b = __float2bfloat16_rn(s);
-    P.out[(long)(row0 + r) * P.n_out + n] = *reinterpret_cast<const uint16_t*>(&b);
-  }
-  __syncthreads();
+}
+template <int GROUP>
+__device__ __forceinline__ void load_scales(const uint8_t* sc, int i, int lane, float (&s)[8],
+                                            float) {
+  const float4* p =
+      reinterpret_cast<const float4*>(sc + (i * 32 / GROUP) * 256 + (lane / 4) * 32);
+  const float4 a = p[0], b = p[1];
+  s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w;
+  s[4] = b.x, s[5] = b.y, s[6] = b.z, s[7] = b.w;
 }
 
-constexpr int kMaxNT = 2;  // 16 sorted rows per pass over the expert's weights
+// The lane's x of step i of a unit: x4[t] the lane's row of tile t at the
+// unit's first column + 8 (lane % 4); n8: 16-byte pieces of a row from the
+// unit's first column to d (columns past d are 0: their weights are 0, but 0
+// times what lies there need not be).
+template <int NT>
+__device__ __forceinline__ void load_x(const uint4* const (&x4)[NT], int i, int n8, int lane,
+                                       uint4 (&xv)[NT]) {
+  if (n8 >= kCols / 8) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xv[t] = __ldg(x4[t] + 4 * i);
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      xv[t] = 4 * i + lane % 4 < n8 ? __ldg(x4[t] + 4 * i) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// 32 columns (step i) of one unit (at w) times NT * 8 rows of x.
+template <int GROUP, typename S, int NT>
+__device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const uint4 (&xv)[NT],
+                                     float (&acc)[4][NT][4]) {
+  const uint4 w0 = *reinterpret_cast<const uint4*>(w + 1024 * i + 16 * lane);
+  const uint4 w1 = *reinterpret_cast<const uint4*>(w + 1024 * i + 512 + 16 * lane);
+  float s[8];
+  load_scales<GROUP>(w + kWeightBytes, i, lane, s, S{});
+  const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
+  const uint32_t off = 0xc1c0c1c0u;  // -24
+  const uint32_t o4[4] = {off, off, off, off};
+  float z[NT][4];  // -24 * sum of x over the step's columns
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    mma16816(z[t], o4, xv[t].x, xv[t].y, 0.f, 0.f, 0.f, 0.f);
+    mma16816(z[t], o4, xv[t].z, xv[t].w, z[t][0], z[t][1], z[t][2], z[t][3]);
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint32_t a[4] = {widen2(wa[m], 0), widen2(wb[m], 0), widen2(wa[m], 1),
+                           widen2(wb[m], 1)};
+    const uint32_t b[4] = {widen2(wa[m], 2), widen2(wb[m], 2), widen2(wa[m], 3),
+                           widen2(wb[m], 3)};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float c[4];
+      mma16816(c, a, xv[t].x, xv[t].y, z[t][0], z[t][1], z[t][2], z[t][3]);
+      mma16816(c, b, xv[t].z, xv[t].w, c[0], c[1], c[2], c[3]);
+      acc[m][t][0] = fmaf(s[2 * m], c[0], acc[m][t][0]);
+      acc[m][t][1] = fmaf(s[2 * m], c[1], acc[m][t][1]);
+      acc[m][t][2] = fmaf(s[2 * m + 1], c[2], acc[m][t][2]);
+      acc[m][t][3] = fmaf(s[2 * m + 1], c[3], acc[m][t][3]);
+    }
+  }
+}
+
+// What the CTA shares.
+constexpr int kRedLane = 17;  // floats per lane (one more than 16: no bank conflicts)
+constexpr int kRed = kWarps * 32 * kRedLane;
+struct Shared {
+  uint64_t bars[kWarps][kStages];
+  int wsum[kWarps];
+  int abort;
+  int* first;  // [N_r + 1] passes of xr rows before expert e
+  int* off;    // [N_r + 1] the experts' segments
+  float* red;  // [2][kRed]
+};
+// Dynamic shared memory: the rings, the sums, the two arrays.
+inline int smem_bytes(int unit_bytes, int N_r) {
+  return kWarps * kStages * unit_bytes + 2 * kRed * 4 + 2 * (N_r + 1) * 4;
+}
+
+// A warp's walk over its units: item after item, its columns of each.
+struct Walk {
+  long item;
+  int e, row0, rows, tile, kb;
+};
+
+// Item -> expert (the last e with first[e] <= pass), rows, tile.
+__device__ __forceinline__ void find(const Params& P, const Shared& sh, Walk& k) {
+  const int pass = (int)(k.item / P.tiles);
+  k.tile = (int)(k.item % P.tiles);
+  int lo = 0, hi = P.N_r - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sh.first[mid] <= pass) lo = mid;
+    else hi = mid - 1;
+  }
+  k.e = lo;
+  k.row0 = sh.off[lo] + (pass - sh.first[lo]) * P.xr;
+  k.rows = min(sh.off[lo + 1] - k.row0, P.xr);
+}
 
 template <int GROUP, typename S>
 __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) {
-  __shared__ int found[3];
-  __shared__ int tok[8 * kMaxNT];
-  __shared__ __align__(16) float red[kWarps * kMaxNT * 8 * kMT * kRows];
-  const int tid = threadIdx.x;
+  extern __shared__ __align__(128) uint8_t ring[];  // [kWarps][kStages][unit_bytes]
+  __shared__ Shared sh;
+  volatile int* abort = &sh.abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = P.T * P.k;
-  if (tid == 0) found[0] = -1;
-  __syncthreads();
-  if (P.rows_mode) {
-    const int j = blockIdx.y;
-    for (int e = tid; e < P.N_r; e += kThreads) {
-      const int a = P.offsets[e], b = P.offsets[e + 1];
-      if (a == j && b > a) {
-        found[0] = e;
-        found[1] = a;
-        found[2] = b < n ? b : n;
-      }
-    }
-  } else if (tid == 0) {
-    const int e = blockIdx.y;
-    const int a = P.offsets[e], b = P.offsets[e + 1];
-    if (b > a && a >= 0) {
-      found[0] = e;
-      found[1] = a;
-      found[2] = b < n ? b : n;
-    }
+  if (tid < kWarps * kStages) mbar_init(smem_u32(&sh.bars[0][0] + tid), 1);
+  if (tid == 0) {
+    sh.abort = 0;
+    sh.red = reinterpret_cast<float*>(ring + kWarps * kStages * P.unit_bytes);
+    sh.first = reinterpret_cast<int*>(sh.red + 2 * kRed);
+    sh.off = sh.first + P.N_r + 1;
   }
   __syncthreads();
-  const int e = found[0];
-  if (e < 0) return;
-  const int begin = found[1], end = found[2];
-  const int mt0 = blockIdx.x * kMT;
-  const int n_mt = P.MT - mt0 < kMT ? P.MT - mt0 : kMT;
-  for (int row0 = begin; row0 < end; row0 += 8 * kMaxNT) {
-    const int rows = end - row0 < 8 * kMaxNT ? end - row0 : 8 * kMaxNT;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  for (int e = tid; e <= P.N_r; e += kThreads) sh.off[e] = min(max(P.offsets[e], 0), n);
+  __syncthreads();
+  {  // exclusive scan of the experts' passes (thread i owns experts [i c, i c + c))
+    auto passes = [&](int e) {
+      const int rows = sh.off[e + 1] - sh.off[e];
+      return rows > 0 ? (rows + P.xr - 1) / P.xr : 0;
+    };
+    const int c = (P.N_r + kThreads - 1) / kThreads;
+    const int e0 = tid * c, e1 = e0 + c < P.N_r ? e0 + c : P.N_r;
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += passes(e);
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh.wsum[warp] = x;
     __syncthreads();
-    if (tid < rows) {
-      int t = row0 + tid;
+    int before = x - mine;
+    for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+    for (int e = e0; e < e1; ++e) {
+      sh.first[e] = before;
+      before += passes(e);
+    }
+    if (e0 < P.N_r && e1 == P.N_r) sh.first[P.N_r] = before;
+  }
+  __syncthreads();
+  const long items = (long)sh.first[P.N_r] * P.tiles;
+
+  // ---- the warp's ring ---------------------------------------------------------
+  uint8_t* slots = ring + warp * kStages * P.unit_bytes;
+  Walk ahead;  // the next unit to request
+  ahead.item = warp < P.KB ? (long)blockIdx.x : items;
+  ahead.kb = warp;
+  const uint8_t* src = nullptr;
+  const long stride = (long)kWarps * P.unit_bytes;
+  auto start = [&]() {
+    if (ahead.item >= items) return;
+    find(P, sh, ahead);
+    src = P.wp + (((long)ahead.e * P.tiles + ahead.tile) * P.KB + warp) * (long)P.unit_bytes;
+  };
+  start();
+  int requested = 0, used = 0;
+  auto request = [&]() {  // whole warp
+    if (ahead.item >= items) return;
+    const int s = requested % kStages;
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&sh.bars[warp][s]);
+      mbar_arrive_expect_tx(bar, (uint32_t)P.unit_bytes);
+      eg::bulk_load(smem_u32(slots + s * P.unit_bytes), src, (uint32_t)P.unit_bytes, bar);
+    }
+    ++requested;
+    ahead.kb += kWarps;
+    src += stride;
+    if (ahead.kb >= P.KB) {
+      ahead.kb = warp;
+      ahead.item += gridDim.x;
+      start();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) request();
+
+  bool go = true;
+  int par = 0;
+  auto run = [&](auto nt, const Walk& k) {
+    constexpr int NT = decltype(nt)::value;
+    const uint4* x4[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      // a lane without a row reads the item's first one; its results are dropped
+      const int r = t * 8 + lane / 4;
+      int tok = k.row0 + (r < k.rows ? r : 0);
       if (P.perm) {
-        const int p = P.perm[row0 + tid];
-        t = p >= 0 && p < n ? p / P.k : -1;
-        if (t < 0) mr_raise(MR_FLAG_BAD_INDEX);
+        const int p = P.perm[tok];
+        tok = p >= 0 && p < n ? p / P.k : 0;
+        if (p < 0 || p >= n) mr_raise(MR_FLAG_BAD_INDEX);
       }
-      tok[tid] = t;
+      x4[t] = reinterpret_cast<const uint4*>(P.x + (long)tok * P.d) + lane % 4 +
+              warp * (kCols / 8);
     }
-    __syncthreads();
-    if (rows <= 8) pass<GROUP, S, 1>(P, e, mt0, n_mt, row0, rows, tok, red);
-    else pass<GROUP, S, 2>(P, e, mt0, n_mt, row0, rows, tok, red);
+    float acc[4][NT][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
+    uint4 xn[4][NT];
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_x<NT>(x4, i, warp < P.KB ? P.d / 8 - warp * (kCols / 8) : 0, lane, xn[i]);
+    }
+    for (int kb = warp; kb < P.KB; kb += kWarps) {
+      const int s = used % kStages, n8 = P.d / 8 - kb * (kCols / 8);
+      const uint8_t* w = slots + s * P.unit_bytes;
+      const uint32_t bar = smem_u32(&sh.bars[warp][s]), ph = (uint32_t)(used / kStages) & 1u;
+      if constexpr (NT == 1) {  // x runs one unit ahead
+        uint4 xc[4][NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xc[i][0] = xn[i][0];
+        if (kb + kWarps < P.KB) {
+          x4[0] += kWarps * (kCols / 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_x<NT>(x4, i, n8 - kWarps * (kCols / 8), lane, xn[i]);
+        }
+        go = go && __all_sync(0xffffffffu, mbar_wait(bar, ph, abort));
+        if (!go) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) step<GROUP, S, NT>(w, i, lane, xc[i], acc);
+      } else {  // the unit's x is on its way while the weights arrive
+        uint4 xv[4][NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_x<NT>(x4, i, n8, lane, xv[i]);
+        go = go && __all_sync(0xffffffffu, mbar_wait(bar, ph, abort));
+        if (!go) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) step<GROUP, S, NT>(w, i, lane, xv[i], acc);
+      }
+      __syncwarp();
+      ++used;
+      request();
+      if constexpr (NT > 1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          x4[t] += kWarps * (kCols / 8);
+      }
+    }
+    // the warps' sums meet, one tile of 8 rows of x at a time: acc 0, 1 are rows
+    // 2 (lane % 4), + 1 of x against output row 16 m + lane / 4; acc 2, 3 the
+    // same against 16 m + 8 + lane / 4
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* red = sh.red + par * kRed;  // the other half is still being read
+      par ^= 1;
+      float* mine = red + (warp * 32 + lane) * kRedLane;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[4 * m + i] = acc[m][t][i];
+      __syncthreads();
+      for (int o = tid; o < 8 * kTile; o += kThreads) {
+        const int c = o / kTile, r = o % kTile;
+        const float* src = red + ((r % 8) * 4 + c / 2) * kRedLane + 4 * (r / 16) + (c & 1) +
+                           2 * ((r / 8) & 1);
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += src[w * 32 * kRedLane];
+        const int row = t * 8 + c, col = k.tile * kTile + r;
+        if (row < k.rows && col < P.n_out && !*abort) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(v);
+          P.out[(long)(k.row0 + row) * P.n_out + col] = *reinterpret_cast<const uint16_t*>(&b);
+        }
+      }
+    }
+  };
+  for (long it = blockIdx.x; it < items; it += gridDim.x) {
+    Walk k;
+    k.item = it;
+    find(P, sh, k);
+    if (k.rows <= 8) run(std::integral_constant<int, 1>{}, k);
+    else run(std::integral_constant<int, 2>{}, k);
   }
+  // after a give-up: every requested copy lands before the CTA exits
+  if (lane == 0)
+    for (; used < requested; ++used)
+      mbar_wait(smem_u32(&sh.bars[warp][used % kStages]), (uint32_t)(used / kStages) & 1u, abort,
+                true);
 }
 
 }  // namespace w4

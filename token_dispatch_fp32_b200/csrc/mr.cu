@@ -1686,8 +1686,12 @@ int check_w4(int N_r, int n_out, int d, int group, int scale_dtype) {
 }
 
 template <int GROUP, typename S>
-int launch_expert_w4(const mr::w4::Params& P, dim3 grid, cudaStream_t s) {
-  mr::w4::expert_w4_kernel<GROUP, S><<<grid, mr::w4::kThreads, 0, s>>>(P);
+int launch_expert_w4(const mr::w4::Params& P, unsigned grid, cudaStream_t s) {
+  auto kern = mr::w4::expert_w4_kernel<GROUP, S>;
+  const int smem = mr::w4::smem_bytes(P.unit_bytes, P.N_r);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return MR_ERR_CUDA;
+  kern<<<grid, mr::w4::kThreads, (size_t)smem, s>>>(P);
   return launch_status();
 }
 
@@ -1703,19 +1707,17 @@ int mr_expert_pack_w4(const void* q, const void* scales, int scale_dtype, int N_
   const mr::w4::Layout l = mr::w4::make_layout(N_r, n_out, d, group, sb);
   if (!q || !scales || !packed || packed_bytes < l.total) return MR_ERR_INVALID_ARG;
   if (!aligned16(packed)) return MR_ERR_UNSUPPORTED;
-  const long ctas = (l.blocks + 7) / 8;
-  if (ctas >= (1LL << 31)) return MR_ERR_UNSUPPORTED;
+  const long units = (long)N_r * l.tiles * l.KB;
+  if (units >= (1LL << 31)) return MR_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint4* wp = static_cast<uint4*>(packed);
-  void* sp = static_cast<char*>(packed) + l.scale_off;
   if (sb == 2)
-    mr::w4::w4_pack_kernel<uint16_t><<<(unsigned)ctas, 256, 0, s>>>(
+    mr::w4::w4_pack_kernel<uint16_t><<<(unsigned)units, 128, 0, s>>>(
         static_cast<const uint8_t*>(q), static_cast<const uint16_t*>(scales), n_out, d, group,
-        l.MT, l.KB, l.blocks, wp, static_cast<uint16_t*>(sp));
+        l.tiles, l.KB, l.unit_bytes, static_cast<uint8_t*>(packed));
   else
-    mr::w4::w4_pack_kernel<float><<<(unsigned)ctas, 256, 0, s>>>(
-        static_cast<const uint8_t*>(q), static_cast<const float*>(scales), n_out, d, group, l.MT,
-        l.KB, l.blocks, wp, static_cast<float*>(sp));
+    mr::w4::w4_pack_kernel<float><<<(unsigned)units, 128, 0, s>>>(
+        static_cast<const uint8_t*>(q), static_cast<const float*>(scales), n_out, d, group,
+        l.tiles, l.KB, l.unit_bytes, static_cast<uint8_t*>(packed));
   return launch_status();
 }
 
@@ -1734,21 +1736,23 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   P.x = static_cast<const uint16_t*>(x);
   P.perm = perm;
   P.offsets = offsets;
-  P.wp = static_cast<const uint4*>(packed);
-  P.sp = static_cast<const char*>(packed) + l.scale_off;
+  P.wp = static_cast<const uint8_t*>(packed);
   P.out = static_cast<uint16_t*>(out);
   P.T = T;
   P.d = d;
   P.k = k;
   P.N_r = N_r;
   P.n_out = n_out;
-  P.MT = l.MT;
+  P.tiles = l.tiles;
   P.KB = l.KB;
-  // fewer sorted rows than experts: count the rows, so that one token does not
-  // launch a CTA for every expert it did not choose
-  P.rows_mode = (long)T * k < N_r ? 1 : 0;
-  const dim3 grid((unsigned)((l.MT + mr::w4::kMT - 1) / mr::w4::kMT),
-                  (unsigned)(P.rows_mode ? T * k : N_r));
+  P.unit_bytes = l.unit_bytes;
+  int sms = 0, cc = 0;
+  if (!device_info(&sms, &cc)) return MR_ERR_CUDA;
+  // rows of x per pass over an expert's weights
+  const long n = (long)T * k;
+  P.xr = mr::w4::kRowsPerPass;
+  const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
+  const unsigned grid = (unsigned)std::min<long>(items, 2l * sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (sb == 2) {
     if (group == 32) return launch_expert_w4<32, uint16_t>(P, grid, s);
