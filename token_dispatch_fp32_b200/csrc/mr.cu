@@ -1455,7 +1455,7 @@ int launch_dx_slots(const void* W, const int32_t* idx, const float* slot, const 
                     void* dx, int T, int d, int N_r, int k, int sms, cudaStream_t s) {
   constexpr int CW = 32 * CPL;
   auto kern = mr::rb::dx_slots_kernel<CPL, VEC, BF16, WBF16>;
-  const size_t smem = (size_t)(N_r + 1) * CW * sizeof(float) + mr::rb::kDxPairs * sizeof(int2);
+  const size_t smem = mr::rb::dx_smem_bytes(N_r, CW, k);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return MR_ERR_CUDA;
@@ -1481,8 +1481,8 @@ template <bool BF16, bool WBF16>
 int launch_dx(const void* W, const int32_t* idx, const float* slot, const void* add, void* dx,
               int T, int d, int N_r, int k, int sms, cudaStream_t s) {
   const bool vec = d % 4 == 0 && aligned16(dx) && (!add || aligned16(add));
-  // 128 columns of every expert when they fit shared memory (N_r <= 432), else 64
-  if (((size_t)N_r + 1) * 128 * sizeof(float) + mr::rb::kDxPairs * sizeof(int2) <= 232448) {
+  // 128 columns of every expert when they fit shared memory (N_r <= 436 at k = 8), else 64
+  if (mr::rb::dx_smem_bytes(N_r, 128, k) <= 232448) {
     if (vec)
       return launch_dx_slots<4, true, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
     return launch_dx_slots<4, false, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);

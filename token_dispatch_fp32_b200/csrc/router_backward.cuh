@@ -106,27 +106,57 @@ __global__ void __launch_bounds__(32 * kDlWarps)
 //
 // A CTA keeps CW = 32 * CPL columns of every expert's row of W (fp32, plus one
 // row of zeros for ids out of range) in shared memory and walks a range of
-// tokens, one warp per token (addv may be dxv: neither is __restrict__): each slot is one conflict-free read of its
-// expert's CW columns and CPL fused multiply-adds per lane.  The k * d reads
-// of W per token then come from shared memory (128 bytes a cycle and SM)
-// instead of L2, which is what bounds the kernel.  The tokens' (row, dl) pairs
-// are staged kDxBatch tokens at a time.
+// tokens: each slot is one conflict-free read of its expert's CW columns and
+// CPL fused multiply-adds per lane.  The k * d reads of W per token then come
+// from shared memory (128 bytes a cycle and SM), which is what bounds the
+// kernel, instead of L2.  A warp takes kDxTokens tokens at a time (independent
+// reads in flight) and stages their (row, dl) pairs in its own piece of shared
+// memory, the next tokens' already on their way (addv may be dxv: neither is
+// __restrict__).
 constexpr int kDxThreads = 512;
-constexpr int kDxPairs = 1024;  // (row, dl) pairs per batch
+constexpr int kDxTokens = 4;
+constexpr int kDxPairs = kDxTokens * kMaxK;  // (row, dl) pairs a warp stages, twice
+
+__host__ __device__ constexpr size_t dx_smem_bytes(int N_r, int cw, int k) {
+  // two buffers per warp of kDxTokens rows of pairs, each padded to an even count
+  return ((size_t)N_r + 1) * cw * 4 + (size_t)(kDxThreads / 32) * 2 * kDxTokens * ((k + 1) & ~1) * 8;
+}
 
 template <int CPL, bool VEC, bool BF16, bool WBF16>
 __global__ void __launch_bounds__(kDxThreads)
     dx_slots_kernel(const void* __restrict__ Wv, const int32_t* __restrict__ idx,
-                    const float* __restrict__ slot, const void* addv, void* dxv, int T, int d, int N_r, int k, int tokens_per_cta) {
+                    const float* __restrict__ slot, const void* addv, void* dxv, int T, int d,
+                    int N_r, int k, int tokens_per_cta) {
   constexpr int CW = 32 * CPL;
-  extern __shared__ __align__(16) float sm[];
-  float* Ws = sm;                                            // [N_r + 1][CW]
-  int2* pairs = reinterpret_cast<int2*>(sm + (N_r + 1) * CW);  // [kDxPairs]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int U = kDxTokens;
   constexpr int kWarps = kDxThreads / 32;
+  constexpr int kRegs = kDxPairs / 32;
+  extern __shared__ __align__(16) float sm[];
+  float* Ws = sm;  // [N_r + 1][CW]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kp = (k + 1) & ~1;
+  int2* pairs = reinterpret_cast<int2*>(sm + (N_r + 1) * CW) + warp * 2 * U * kp;  // [2][U][kp]
   const int c0 = blockIdx.x * CW;
   const long t_begin = (long)blockIdx.y * tokens_per_cta;
   const long t_end = t_begin + tokens_per_cta < T ? t_begin + tokens_per_cta : T;
+
+  // the pairs of tokens t .. t + U - 1, one per lane and 32: id and dl
+  int er[kRegs];
+  float gr[kRegs];
+  const int used = (U * k + 31) / 32;
+  auto fetch = [&](long t) {
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r) {
+      if (r >= used) break;
+      const int i = lane + 32 * r;
+      const bool in = i < U * k && t + i / k < t_end;
+      er[r] = in ? idx[t * k + i] : -1;
+      gr[r] = in ? slot[t * k + i] : 0.0f;
+    }
+  };
+  long t = t_begin + warp * U;
+  fetch(t);
+  for (int i = lane; i < 2 * U * kp; i += 32) pairs[i] = make_int2(N_r * CW, 0);  // odd k: padding
   for (int i = threadIdx.x; i < (N_r + 1) * CW; i += kDxThreads) {
     const int e = i / CW, c = c0 + i % CW;
     float v = 0.0f;
@@ -136,87 +166,111 @@ __global__ void __launch_bounds__(kDxThreads)
     }
     Ws[i] = v;
   }
+  __syncthreads();
   // columns of this lane: CPL consecutive ones (VEC) or every 32nd
   auto col = [&](int i) { return VEC ? lane * CPL + i : lane + 32 * i; };
-  const int batch = kDxPairs / k;
-  for (long tb = t_begin; tb < t_end; tb += batch) {
-    const int nt = (int)(t_end - tb < batch ? t_end - tb : batch);
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * k; i += kDxThreads) {
-      const int e = idx[tb * k + i];
-      const bool ok = e >= 0 && e < N_r;
-      pairs[i] = make_int2((ok ? e : N_r) * CW, ok ? __float_as_int(slot[tb * k + i]) : 0);
+  const bool mine = c0 + lane * CPL < d;  // VEC: d is a multiple of CPL
+  for (int par = 0; t < t_end; t += kWarps * U, par ^= 1) {
+    int2* buf = pairs + par * U * kp;
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r) {
+      if (r >= used) break;
+      const int i = lane + 32 * r;
+      const bool ok = er[r] >= 0 && er[r] < N_r;
+      if (i < U * k)
+        buf[(i / k) * kp + i % k] =
+            make_int2((ok ? er[r] : N_r) * CW, ok ? __float_as_int(gr[r]) : 0);
     }
-    __syncthreads();
-    for (int q = warp; q < nt; q += kWarps) {
-      float acc[CPL];
+    __syncwarp();
+    fetch(t + kWarps * U);
+    float acc[U][CPL];
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[i] = 0.0f;
-      const int2* p = pairs + q * k;
-#pragma unroll 4
-      for (int j = 0; j < k; ++j) {
-        const int2 pr = p[j];
-        const float a = __int_as_float(pr.y);
-        const float* wr = Ws + pr.x;
-        if constexpr (VEC && CPL == 4) {
-          const float4 wv = *reinterpret_cast<const float4*>(wr + lane * 4);
-          acc[0] = fmaf(a, wv.x, acc[0]);
-          acc[1] = fmaf(a, wv.y, acc[1]);
-          acc[2] = fmaf(a, wv.z, acc[2]);
-          acc[3] = fmaf(a, wv.w, acc[3]);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[u][i] = 0.0f;
+    // add, on its way while the slots are summed
+    uint32_t ab[U][CPL / 2];
+    float af[U][CPL];
+    if (VEC && addv) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= t_end || !mine) continue;
+        const long o = (t + u) * d + c0 + lane * CPL;
+        if constexpr (BF16) {
+          const uint16_t* a = static_cast<const uint16_t*>(addv) + o;
+          if constexpr (CPL == 4)
+            *reinterpret_cast<uint2*>(ab[u]) = *reinterpret_cast<const uint2*>(a);
+          else ab[u][0] = *reinterpret_cast<const uint32_t*>(a);
         } else {
-#pragma unroll
-          for (int i = 0; i < CPL; ++i) acc[i] = fmaf(a, wr[col(i)], acc[i]);
+          const float* a = static_cast<const float*>(addv) + o;
+          if constexpr (CPL == 4)
+            *reinterpret_cast<float4*>(af[u]) = *reinterpret_cast<const float4*>(a);
+          else *reinterpret_cast<float2*>(af[u]) = *reinterpret_cast<const float2*>(a);
         }
       }
-      const long base = (tb + q) * d + c0;
+    }
+#pragma unroll 4
+    for (int j = 0; j < kp; j += 2) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int4 pr = *reinterpret_cast<const int4*>(buf + u * kp + j);
+        const float a0 = __int_as_float(pr.y), a1 = __int_as_float(pr.w);
+        const float *w0 = Ws + pr.x, *w1 = Ws + pr.z;
+        if constexpr (VEC && CPL == 4) {
+          const float4 v0 = *reinterpret_cast<const float4*>(w0 + lane * 4);
+          const float4 v1 = *reinterpret_cast<const float4*>(w1 + lane * 4);
+          acc[u][0] = fmaf(a1, v1.x, fmaf(a0, v0.x, acc[u][0]));
+          acc[u][1] = fmaf(a1, v1.y, fmaf(a0, v0.y, acc[u][1]));
+          acc[u][2] = fmaf(a1, v1.z, fmaf(a0, v0.z, acc[u][2]));
+          acc[u][3] = fmaf(a1, v1.w, fmaf(a0, v0.w, acc[u][3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPL; ++i)
+            acc[u][i] = fmaf(a1, w1[col(i)], fmaf(a0, w0[col(i)], acc[u][i]));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t + u >= t_end) break;
+      const long base = (t + u) * d + c0;
       if constexpr (VEC) {
-        if (c0 + lane * CPL < d) {  // d is a multiple of CPL
-          if constexpr (BF16) {
-            uint32_t o[CPL / 2];
-            if (addv) {
-              const uint32_t* a =
-                  reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(addv) + base) +
-                  lane * (CPL / 2);
+        if (!mine) continue;
+        if constexpr (BF16) {
+          uint32_t o[CPL / 2];
 #pragma unroll
-              for (int i = 0; i < CPL / 2; ++i) {
-                float lo, hi;
-                bf16x2_unpack(a[i], lo, hi);
-                acc[2 * i] += lo;
-                acc[2 * i + 1] += hi;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < CPL / 2; ++i) o[i] = bf16x2_pack_rn(acc[2 * i], acc[2 * i + 1]);
-            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(dxv) + base) +
-                            lane * (CPL / 2);
-            if constexpr (CPL == 4) __stcs(reinterpret_cast<uint2*>(out), make_uint2(o[0], o[1]));
-            else __stcs(out, o[0]);
-          } else {
-            const float* a = addv ? static_cast<const float*>(addv) + base + lane * CPL : nullptr;
-            float* out = static_cast<float*>(dxv) + base + lane * CPL;
-            if (a) {
-#pragma unroll
-              for (int i = 0; i < CPL; ++i) acc[i] += a[i];
-            }
-            if constexpr (CPL == 4)
-              __stcs(reinterpret_cast<float4*>(out), make_float4(acc[0], acc[1], acc[2], acc[3]));
-            else
-              __stcs(reinterpret_cast<float2*>(out), make_float2(acc[0], acc[1]));
+          for (int i = 0; i < CPL / 2; ++i) {
+            float lo = 0.0f, hi = 0.0f;
+            if (addv) bf16x2_unpack(ab[u][i], lo, hi);
+            o[i] = bf16x2_pack_rn(acc[u][2 * i] + lo, acc[u][2 * i + 1] + hi);
           }
+          uint16_t* out = static_cast<uint16_t*>(dxv) + base + lane * CPL;
+          if constexpr (CPL == 4) __stcs(reinterpret_cast<uint2*>(out), make_uint2(o[0], o[1]));
+          else __stcs(reinterpret_cast<uint32_t*>(out), o[0]);
+        } else {
+          float* out = static_cast<float*>(dxv) + base + lane * CPL;
+          if (addv) {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) acc[u][i] += af[u][i];
+          }
+          if constexpr (CPL == 4)
+            __stcs(reinterpret_cast<float4*>(out),
+                   make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]));
+          else __stcs(reinterpret_cast<float2*>(out), make_float2(acc[u][0], acc[u][1]));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
           const int c = col(i);
           if (c0 + c >= d) continue;
+          float v = acc[u][i];
           if constexpr (BF16) {
-            if (addv) acc[i] += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[base + c]);
-            const __nv_bfloat16 b = __float2bfloat16_rn(acc[i]);
+            if (addv) v += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[base + c]);
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
             static_cast<uint16_t*>(dxv)[base + c] = *reinterpret_cast<const uint16_t*>(&b);
           } else {
-            if (addv) acc[i] += static_cast<const float*>(addv)[base + c];
-            static_cast<float*>(dxv)[base + c] = acc[i];
+            if (addv) v += static_cast<const float*>(addv)[base + c];
+            static_cast<float*>(dxv)[base + c] = v;
           }
         }
       }
