@@ -1417,37 +1417,124 @@ int launch_gather_backward(const void* dxs, const int32_t* inv, const void* add,
   return launch_status();
 }
 
-// Workspace of mr_router_backward: the slots' logit gradients, softmax's dense
-// ones, and dW's partial sums (extra pieces of long segments, or K slices).
+// Workspace of mr_router_backward: the slots' logit gradients (sigmoid), or
+// softmax's dense ones, as fp32 and as planes, and W's planes; then dW's partial
+// sums (extra pieces of long segments, or K slices).
 struct RouterBwdWs {
-  size_t slot, dense, part, total;
+  size_t slot, dense, planes, w_planes, part, total;
   int slices;  // K slices of the dense dW product (softmax)
 };
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 RouterBwdWs router_bwd_ws(int T, int d, int N_r, int k, int flags) {
-  RouterBwdWs w;
-  w.slices = 0;
-  w.slot = 0;
-  size_t at = align256((size_t)T * k * sizeof(float));
-  w.dense = at;
+  RouterBwdWs w = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
   if (flags & MR_SCORE_SOFTMAX) {
-    at += align256((size_t)T * N_r * sizeof(float));
-    // slices of at least 512 tokens, up to about four tiles per SM
-    const long tiles = (long)((N_r + mr::rb::kGemmT - 1) / mr::rb::kGemmT) *
-                       ((d + mr::rb::kGemmT - 1) / mr::rb::kGemmT);
-    long z = (4 * 148 + tiles - 1) / tiles;
-    z = std::min<long>(z, T / 512);
-    w.slices = (int)std::max<long>(1, z);
-    w.part = at;
-    if (w.slices > 1) at += (size_t)w.slices * N_r * d * sizeof(float);
+    w.dense = take((size_t)T * N_r * sizeof(float));
+    w.planes = take((size_t)3 * T * ((N_r + 7) & ~7) * 2);
+    w.w_planes = take((size_t)3 * N_r * d * 2);
+    // as many slices of at least 512 tokens as leave the fewest SMs idle in the
+    // last wave of 128 x 256 tiles (148 SMs), at most 8
+    const long tiles = (long)((N_r + mr::tc::BM - 1) / mr::tc::BM) *
+                       ((d + mr::pg::kBN - 1) / mr::pg::kBN);
+    double best = 0;
+    for (int z = 1; z <= 8 && (z == 1 || T / z >= 512); ++z) {
+      const long waves = (tiles * z + 147) / 148;
+      const double eff = (double)(tiles * z) / (waves * 148);
+      if (z == 1 || eff > best + 0.02) {
+        best = eff;
+        w.slices = z;
+      }
+    }
+    w.part = take(w.slices > 1 ? (size_t)w.slices * N_r * d * sizeof(float) : 0);
   } else {
-    w.part = at;
-    at += (size_t)((long)T * k / mr::rb::kDwRows) * d * sizeof(float);
+    w.slot = take((size_t)T * k * sizeof(float));
+    w.part = take((size_t)((long)T * k / mr::rb::kDwRows) * d * sizeof(float));
   }
   w.total = at;
   return w;
+}
+
+// bf16 [planes][rows][cols] (rows `pitch` elements apart), box box_cols x box_rows.
+bool make_map_planes(CUtensorMap* map, const void* base, int cols, int rows, int planes, int pitch,
+                     int box_cols, int box_rows, CUtensorMapSwizzle sw) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * rows};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool DW, int NPB, bool OBF16>
+int launch_planes(const CUtensorMap& ma, const CUtensorMap& mb, const mr::pg::GemmParams& P,
+                  int sms, cudaStream_t s) {
+  auto kern = mr::pg::planes_gemm_kernel<DW, NPB, OBF16>;
+  const int smem = (int)mr::pg::smem_bytes(NPB);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return MR_ERR_CUDA;
+  const int items = P.m_tiles * P.n_tiles * P.splits;
+  kern<<<(unsigned)std::min(items, sms), mr::tc::kThreads, (size_t)smem, s>>>(ma, mb, P);
+  return launch_status();
+}
+
+mr::pg::GemmParams gemm_params(int M, int N, int K, int splits, const void* add, void* out) {
+  mr::pg::GemmParams P;
+  P.M = M;
+  P.N = N;
+  P.K = K;
+  P.m_tiles = (M + mr::tc::BM - 1) / mr::tc::BM;
+  P.n_tiles = (N + mr::pg::kBN - 1) / mr::pg::kBN;
+  P.splits = splits;
+  P.add = add;
+  P.out = out;
+  return P;
+}
+
+// dx = dL . W on the tensor cores, from dL's planes (W fp32: its planes go to
+// w_planes first).
+int launch_dx_planes(const void* planes, const void* W, bool wb, void* w_planes, const void* add,
+                     void* dx, bool xb, int T, int d, int N_r, int sms, cudaStream_t s) {
+  const int Np = (N_r + 7) & ~7;
+  if (!wb) {
+    const long n = (long)N_r * d;
+    mr::tc::split_planes_kernel<<<(unsigned)std::min<long>((n / 8 + 255) / 256, 1 << 20), 256, 0,
+                                  s>>>(static_cast<const float*>(W),
+                                       static_cast<__nv_bfloat16*>(w_planes), n);
+    if (launch_status() != MR_OK) return MR_ERR_CUDA;
+  }
+  CUtensorMap ma, mb;
+  if (!make_map_planes(&ma, planes, Np, T, 3, Np, mr::pg::kBK, mr::tc::BM,
+                       CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map_planes(&mb, wb ? W : w_planes, d, N_r, wb ? 1 : 3, d, 64, mr::pg::kBK,
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+    return MR_ERR_CUDA;
+  const auto P = gemm_params(T, d, N_r, 1, add, dx);
+  if (wb)
+    return xb ? launch_planes<false, 1, true>(ma, mb, P, sms, s)
+              : launch_planes<false, 1, false>(ma, mb, P, sms, s);
+  return xb ? launch_planes<false, 3, true>(ma, mb, P, sms, s)
+            : launch_planes<false, 3, false>(ma, mb, P, sms, s);
+}
+
+// dW = dL^T . x on the tensor cores (x bf16), in `slices` K slices.
+int launch_dw_planes(const void* planes, const void* x, float* out, int T, int d, int N_r,
+                     int slices, int sms, cudaStream_t s) {
+  const int Np = (N_r + 7) & ~7;
+  CUtensorMap ma, mb;
+  if (!make_map_planes(&ma, planes, Np, T, 3, Np, 64, mr::pg::kBK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_planes(&mb, x, d, T, 1, d, 64, mr::pg::kBK, CU_TENSOR_MAP_SWIZZLE_128B))
+    return MR_ERR_CUDA;
+  return launch_planes<true, 1, false>(ma, mb, gemm_params(N_r, d, T, slices, nullptr, out), sms, s);
 }
 
 template <int CPL, bool VEC, bool BF16, bool WBF16>
@@ -1614,37 +1701,52 @@ int mr_router_backward(const void* x, int x_dtype, const void* W, int W_dtype,
   if (!device_info(&sms, &cc)) return MR_ERR_CUDA;
   char* base = static_cast<char*>(workspace);
   float* slot = reinterpret_cast<float*>(base + ws.slot);
-  float* dense = dlogits ? dlogits : softmax ? reinterpret_cast<float*>(base + ws.dense) : nullptr;
   float* part = reinterpret_cast<float*>(base + ws.part);
+  const bool xb = x_dtype == MR_BF16, wb = W_dtype == MR_BF16;
   const float eps = (flags & MR_NORM_NO_EPS) ? 0.0f : mr::rb::kEps;
   const unsigned gt = (unsigned)((T + mr::rb::kDlWarps - 1) / mr::rb::kDlWarps);
-  if (softmax)
+  if (softmax) {
+    // dense products: on the tensor cores where TMA takes the rows (16-byte
+    // multiples; dW needs bf16 x), else on the CUDA cores
+    const bool rows16 = cc == 10 && d % 8 == 0;
+    const bool dx_tc = dx && rows16 && aligned16(W) && aligned16(dx) && (!add || aligned16(add));
+    const bool dw_tc = dW && rows16 && xb && aligned16(x) && aligned16(dW);
+    float* dense = dlogits ? dlogits
+                   : (dx && !dx_tc) || (dW && !dw_tc) ? reinterpret_cast<float*>(base + ws.dense)
+                                                      : nullptr;
+    __nv_bfloat16* planes =
+        dx_tc || dw_tc ? reinterpret_cast<__nv_bfloat16*>(base + ws.planes) : nullptr;
     mr::rb::dlogits_kernel<true><<<gt, 32 * mr::rb::kDlWarps, 0, s>>>(
-        logits, idx, dw, T, N_r, k, route_scale, eps, slot, dense);
-  else
-    mr::rb::dlogits_kernel<false><<<gt, 32 * mr::rb::kDlWarps, 0, s>>>(
-        logits, idx, dw, T, N_r, k, route_scale, eps, slot, dense);
+        logits, idx, dw, T, N_r, k, route_scale, eps, nullptr, dense, planes);
+    int rc = launch_status();
+    if (rc != MR_OK) return rc;
+    if (dx) {
+      rc = dx_tc ? launch_dx_planes(planes, W, wb, base + ws.w_planes, add, dx, xb, T, d, N_r, sms, s)
+                 : launch_dense<false>(dense, W, wb, add, dx, xb, T, d, N_r, 1, s);
+      if (rc != MR_OK) return rc;
+    }
+    if (!dW) return MR_OK;
+    float* out = ws.slices > 1 ? part : dW;
+    rc = dw_tc ? launch_dw_planes(planes, x, out, T, d, N_r, ws.slices, sms, s)
+               : launch_dense<true>(dense, x, xb, nullptr, out, false, N_r, d, T, ws.slices, s);
+    if (rc != MR_OK || ws.slices <= 1) return rc;
+    const long n = (long)N_r * d;
+    const unsigned grid = (unsigned)std::min<long>((n + 255) / 256, (long)sms * 16);
+    mr::rb::sum_slices_kernel<<<grid, 256, 0, s>>>(part, ws.slices, n, dW);
+    return launch_status();
+  }
+  mr::rb::dlogits_kernel<false><<<gt, 32 * mr::rb::kDlWarps, 0, s>>>(
+      logits, idx, dw, T, N_r, k, route_scale, eps, slot, dlogits, nullptr);
   int rc = launch_status();
   if (rc != MR_OK) return rc;
-  const bool xb = x_dtype == MR_BF16, wb = W_dtype == MR_BF16;
   if (dx) {
-    if (softmax) rc = launch_dense<false>(dense, W, wb, add, dx, xb, T, d, N_r, 1, s);
-    else if (xb)
+    if (xb)
       rc = wb ? launch_dx<true, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
               : launch_dx<true, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
     else
       rc = wb ? launch_dx<false, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
               : launch_dx<false, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
     if (rc != MR_OK) return rc;
-  }
-  if (dW && softmax) {
-    rc = launch_dense<true>(dense, x, xb, nullptr, ws.slices > 1 ? part : dW, false, N_r, d, T,
-                            ws.slices, s);
-    if (rc != MR_OK || ws.slices <= 1) return rc;
-    const long n = (long)N_r * d;
-    const unsigned grid = (unsigned)std::min<long>((n + 255) / 256, (long)sms * 16);
-    mr::rb::sum_slices_kernel<<<grid, 256, 0, s>>>(part, ws.slices, n, dW);
-    return launch_status();
   }
   if (dW) {
     const int n = T * k;

@@ -18,6 +18,7 @@
 
 #include "combine.cuh"
 #include "mr_common.cuh"
+#include "planes_gemm.cuh"
 #include "rows_backward.cuh"
 
 namespace mr {
@@ -47,14 +48,16 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // One warp per token.  Sigmoid: slot[t*k + j] = dl_j (0 for an id outside
-// [0, N_r)); `dense` (optional) gets the whole row dL[t].  Softmax: `dense`
-// is required and slot is not written.
+// [0, N_r)); `dense` (optional) gets the whole row dL[t].  Softmax: slot is not
+// written; `dense` gets the row and `planes` its three bf16 planes [3][T][Np]
+// (Np = N_r rounded up to 8, the padding 0), either may be null.
 constexpr int kDlWarps = 4;
 template <bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kDlWarps)
     dlogits_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                    const float* __restrict__ g, int T, int N_r, int k, float scale, float eps,
-                   float* __restrict__ slot, float* __restrict__ dense) {
+                   float* __restrict__ slot, float* __restrict__ dense,
+                   __nv_bfloat16* __restrict__ planes) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long t = (long)blockIdx.x * kDlWarps + warp;
   if (t >= T) return;
@@ -95,10 +98,20 @@ __global__ void __launch_bounds__(32 * kDlWarps)
       const float gg = __shfl_sync(0xffffffffu, gj, j);
       if (ok && j != lane && ej == e) gs += gg;
     }
-    for (int i = lane; i < N_r; i += 32)
-      dense[t * N_r + i] = -scale * (expf(L[i] - mx) * inv) * mean;
+    const int Np = (N_r + 7) & ~7;
+    auto put = [&](int i, float v) {
+      if (dense && i < N_r) dense[t * N_r + i] = v;
+      if (planes) {
+        __nv_bfloat16 p[3];
+        tc::split3(v, p[0], p[1], p[2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) planes[((long)q * T + t) * Np + i] = p[q];
+      }
+    };
+    for (int i = lane; i < Np; i += 32)
+      put(i, i < N_r ? -scale * (expf(L[i] - mx) * inv) * mean : 0.0f);
     __syncwarp();
-    if (ok) dense[t * N_r + e] = scale * pj * (gs - mean);  // equal ids write equal values
+    if (ok) put(e, scale * pj * (gs - mean));  // equal ids write equal values
   }
 }
 
