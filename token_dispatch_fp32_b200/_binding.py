@@ -122,7 +122,7 @@ def _check(fn: str, status: int) -> None:
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -136,20 +136,31 @@ def _call(fn: str, dev, stream, *args) -> None:
     stream handle as the last argument: the library launches on the current
     device, so the tensors' device is made current for the call.  `stream`
     (default: that device's current stream) must belong to the same device."""
-    with torch.cuda.device(dev):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
-        _check(fn, getattr(lib(), fn)(*args, C.c_void_p(stream.cuda_stream)))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
+    status = getattr(_lib or lib(), fn)(*args, handle)
+    if status != MR_OK:
+        raise MRError(fn, status)
 
 
 def _device_of(*tensors):
     """The one CUDA device of the given tensors (None entries ignored)."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors must be on one CUDA device, got {sorted(map(str, devs))}")
-    return devs.pop()
+    dev = None
+    for t in tensors:
+        if t is None or t.device == dev:
+            continue
+        if dev is not None:
+            devs = sorted({str(t.device) for t in tensors if t is not None})
+            raise ValueError(f"tensors must be on one CUDA device, got {devs}")
+        dev = t.device
+    return dev
 
 
 def _need(t, name, dtype=None, shape=None):
@@ -159,7 +170,7 @@ def _need(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -496,11 +507,11 @@ def mr_combine_backward(dy, expert_out, w, inv_perm, dexpert=None, dw=None, want
     if dexpert is not None:
         _need(dexpert, "dexpert", dy.dtype, (T * k, d))
     elif want_dexpert:
-        dexpert = torch.empty((T * k, d), dtype=dy.dtype, device=dy.device)
+        dexpert = dy.new_empty((T * k, d))
     if dw is not None:
         _need(dw, "dw", torch.float32, (T, k))
     elif want_dw:
-        dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        dw = torch.empty_like(w)
     if dw is not None and expert_out is None:
         raise ValueError("dw needs expert_out")
     _call("mr_combine_backward", _device_of(dy, expert_out, w, inv_perm, dexpert, dw), stream,
@@ -521,7 +532,7 @@ def mr_gather_rows_backward(dxs, k, inv_perm, add=None, dx=None, stream=None):
     _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     if add is not None:
         _need(add, "add", dxs.dtype, (T, d))
-    dx = torch.empty((T, d), dtype=dxs.dtype, device=dxs.device) if dx is None else \
+    dx = dxs.new_empty((T, d)) if dx is None else \
         _need(dx, "dx", dxs.dtype, (T, d))
     _call("mr_gather_rows_backward", _device_of(dxs, inv_perm, add, dx), stream, _ptr(dxs), dt,
           _ptr(inv_perm), _ptr(add), T, d, k, _ptr(dx))
@@ -565,7 +576,7 @@ def mr_router_backward(x, W, logits, idx, dw, perm, offsets, route_scale, flags=
     if dx is not None:
         _need(dx, "dx", x.dtype, (T, d))
     elif want_dx:
-        dx = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x)
     if dW is not None:
         _need(dW, "dW", torch.float32, (N_r, d))
     elif want_dW:

@@ -1537,12 +1537,22 @@ int launch_dw_planes(const void* planes, const void* x, float* out, int T, int d
   return launch_planes<true, 1, false>(ma, mb, gemm_params(N_r, d, T, slices, nullptr, out), sms, s);
 }
 
-template <int CPL, bool VEC, bool BF16, bool WBF16>
-int launch_dx_slots(const void* W, const int32_t* idx, const float* slot, const void* add,
-                    void* dx, int T, int d, int N_r, int k, int sms, cudaStream_t s) {
+struct DxArgs {
+  const void* W;
+  bool wb;
+  const int32_t* idx;
+  const float* slot;
+  const void* add;
+  void* dx;
+  int T, d, N_r, k, sms;
+  cudaStream_t s;
+};
+
+template <int CPL, bool VEC, bool BF16, int KR>
+int launch_dx_slots(const DxArgs& a) {
   constexpr int CW = 32 * CPL;
-  auto kern = mr::rb::dx_slots_kernel<CPL, VEC, BF16, WBF16>;
-  const size_t smem = mr::rb::dx_smem_bytes(N_r, CW, k);
+  auto kern = mr::rb::dx_slots_kernel<CPL, VEC, BF16, KR>;
+  const size_t smem = mr::rb::dx_smem_bytes(a.N_r, CW, a.k);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return MR_ERR_CUDA;
@@ -1551,32 +1561,32 @@ int launch_dx_slots(const void* W, const int32_t* idx, const float* slot, const 
           cudaSuccess ||
       per_sm < 1)
     return MR_ERR_CUDA;
-  // token ranges per column chunk: whole waves of resident CTAs, at least 64
+  // token ranges per column chunk: two waves of resident CTAs, at least 64
   // tokens each (a CTA first loads N_r * CW weights)
-  const int chunks = (d + CW - 1) / CW;
-  const long slots = (long)sms * per_sm;
+  const int chunks = (a.d + CW - 1) / CW;
+  const long slots = (long)a.sms * per_sm;
   long split = std::max<long>(1, slots * 2 / chunks);
-  split = std::min<long>(split, (T + 63) / 64);
-  const int per_cta = (int)((T + split - 1) / split);
-  const unsigned gy = (unsigned)((T + per_cta - 1) / per_cta);
-  kern<<<dim3((unsigned)chunks, gy), mr::rb::kDxThreads, smem, s>>>(W, idx, slot, add, dx, T, d,
-                                                                     N_r, k, per_cta);
+  split = std::min<long>(split, (a.T + 63) / 64);
+  const int per_cta = (int)((a.T + split - 1) / split);
+  const unsigned gy = (unsigned)((a.T + per_cta - 1) / per_cta);
+  kern<<<dim3((unsigned)chunks, gy), mr::rb::kDxThreads, smem, a.s>>>(
+      a.W, a.wb, a.idx, a.slot, a.add, a.dx, a.T, a.d, a.N_r, a.k, per_cta);
   return launch_status();
 }
 
-template <bool BF16, bool WBF16>
-int launch_dx(const void* W, const int32_t* idx, const float* slot, const void* add, void* dx,
-              int T, int d, int N_r, int k, int sms, cudaStream_t s) {
-  const bool vec = d % 4 == 0 && aligned16(dx) && (!add || aligned16(add));
-  // 128 columns of every expert when they fit shared memory (N_r <= 436 at k = 8), else 64
-  if (mr::rb::dx_smem_bytes(N_r, 128, k) <= 232448) {
-    if (vec)
-      return launch_dx_slots<4, true, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
-    return launch_dx_slots<4, false, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
-  }
-  if (vec)
-    return launch_dx_slots<2, true, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
-  return launch_dx_slots<2, false, BF16, WBF16>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+template <int CPL, bool VEC, bool BF16>
+int launch_dx_k(const DxArgs& a) {
+  return a.k <= 8 ? launch_dx_slots<CPL, VEC, BF16, mr::rb::kDxSmall>(a)
+                  : launch_dx_slots<CPL, VEC, BF16, mr::rb::kDxLarge>(a);
+}
+
+template <bool BF16>
+int launch_dx(const DxArgs& a) {
+  const bool vec = a.d % 4 == 0 && aligned16(a.dx) && (!a.add || aligned16(a.add));
+  // 128 columns of every expert when they fit shared memory (N_r <= 419 at k = 8), else 64
+  if (mr::rb::dx_smem_bytes(a.N_r, 128, a.k) <= 232448)
+    return vec ? launch_dx_k<4, true, BF16>(a) : launch_dx_k<4, false, BF16>(a);
+  return vec ? launch_dx_k<2, true, BF16>(a) : launch_dx_k<2, false, BF16>(a);
 }
 
 template <typename V, bool BF16>
@@ -1740,12 +1750,8 @@ int mr_router_backward(const void* x, int x_dtype, const void* W, int W_dtype,
   int rc = launch_status();
   if (rc != MR_OK) return rc;
   if (dx) {
-    if (xb)
-      rc = wb ? launch_dx<true, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
-              : launch_dx<true, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
-    else
-      rc = wb ? launch_dx<false, true>(W, idx, slot, add, dx, T, d, N_r, k, sms, s)
-              : launch_dx<false, false>(W, idx, slot, add, dx, T, d, N_r, k, sms, s);
+    const DxArgs a = {W, wb, idx, slot, add, dx, T, d, N_r, k, sms, s};
+    rc = xb ? launch_dx<true>(a) : launch_dx<false>(a);
     if (rc != MR_OK) return rc;
   }
   if (dW) {

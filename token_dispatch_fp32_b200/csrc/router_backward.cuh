@@ -126,24 +126,25 @@ __global__ void __launch_bounds__(32 * kDlWarps)
 // reads in flight) and stages their (row, dl) pairs in its own piece of shared
 // memory, the next tokens' already on their way (addv may be dxv: neither is
 // __restrict__).
-constexpr int kDxThreads = 512;
+constexpr int kDxThreads = 768;
 constexpr int kDxTokens = 4;
-constexpr int kDxPairs = kDxTokens * kMaxK;  // (row, dl) pairs a warp stages, twice
+// (row, dl) pairs per lane of a warp's tokens: one for k <= 8, else up to four
+constexpr int kDxSmall = (kDxTokens * 8 + 31) / 32, kDxLarge = kDxTokens * kMaxK / 32;
+constexpr int dx_pairs_per_lane(int k) { return k <= 8 ? kDxSmall : kDxLarge; }
 
 __host__ __device__ constexpr size_t dx_smem_bytes(int N_r, int cw, int k) {
   // two buffers per warp of kDxTokens rows of pairs, each padded to an even count
   return ((size_t)N_r + 1) * cw * 4 + (size_t)(kDxThreads / 32) * 2 * kDxTokens * ((k + 1) & ~1) * 8;
 }
 
-template <int CPL, bool VEC, bool BF16, bool WBF16>
+template <int CPL, bool VEC, bool BF16, int kRegs>
 __global__ void __launch_bounds__(kDxThreads)
-    dx_slots_kernel(const void* __restrict__ Wv, const int32_t* __restrict__ idx,
+    dx_slots_kernel(const void* __restrict__ Wv, bool wbf16, const int32_t* __restrict__ idx,
                     const float* __restrict__ slot, const void* addv, void* dxv, int T, int d,
                     int N_r, int k, int tokens_per_cta) {
   constexpr int CW = 32 * CPL;
   constexpr int U = kDxTokens;
   constexpr int kWarps = kDxThreads / 32;
-  constexpr int kRegs = kDxPairs / 32;
   extern __shared__ __align__(16) float sm[];
   float* Ws = sm;  // [N_r + 1][CW]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -153,18 +154,22 @@ __global__ void __launch_bounds__(kDxThreads)
   const long t_begin = (long)blockIdx.y * tokens_per_cta;
   const long t_end = t_begin + tokens_per_cta < T ? t_begin + tokens_per_cta : T;
 
-  // the pairs of tokens t .. t + U - 1, one per lane and 32: id and dl
-  int er[kRegs];
+  // the pairs of tokens t .. t + U - 1: id and dl; pair i of a lane belongs to
+  // token tk[i] (U for none) and goes to place at[i] of the buffer
+  int er[kRegs], tk[kRegs], at[kRegs];
   float gr[kRegs];
-  const int used = (U * k + 31) / 32;
+#pragma unroll
+  for (int r = 0; r < kRegs; ++r) {
+    const int i = lane + 32 * r;
+    tk[r] = i < U * k ? i / k : U;
+    at[r] = tk[r] * kp + i % k;
+  }
   auto fetch = [&](long t) {
 #pragma unroll
     for (int r = 0; r < kRegs; ++r) {
-      if (r >= used) break;
-      const int i = lane + 32 * r;
-      const bool in = i < U * k && t + i / k < t_end;
-      er[r] = in ? idx[t * k + i] : -1;
-      gr[r] = in ? slot[t * k + i] : 0.0f;
+      const bool in = tk[r] < U && t + tk[r] < t_end;
+      er[r] = in ? idx[t * k + lane + 32 * r] : -1;
+      gr[r] = in ? slot[t * k + lane + 32 * r] : 0.0f;
     }
   };
   long t = t_begin + warp * U;
@@ -174,8 +179,8 @@ __global__ void __launch_bounds__(kDxThreads)
     const int e = i / CW, c = c0 + i % CW;
     float v = 0.0f;
     if (e < N_r && c < d) {
-      if constexpr (WBF16) v = mr_bf16_to_f32(static_cast<const uint16_t*>(Wv)[(long)e * d + c]);
-      else v = static_cast<const float*>(Wv)[(long)e * d + c];
+      v = wbf16 ? mr_bf16_to_f32(static_cast<const uint16_t*>(Wv)[(long)e * d + c])
+                : static_cast<const float*>(Wv)[(long)e * d + c];
     }
     Ws[i] = v;
   }
@@ -187,12 +192,9 @@ __global__ void __launch_bounds__(kDxThreads)
     int2* buf = pairs + par * U * kp;
 #pragma unroll
     for (int r = 0; r < kRegs; ++r) {
-      if (r >= used) break;
-      const int i = lane + 32 * r;
       const bool ok = er[r] >= 0 && er[r] < N_r;
-      if (i < U * k)
-        buf[(i / k) * kp + i % k] =
-            make_int2((ok ? er[r] : N_r) * CW, ok ? __float_as_int(gr[r]) : 0);
+      if (tk[r] < U)
+        buf[at[r]] = make_int2((ok ? er[r] : N_r) * CW, ok ? __float_as_int(gr[r]) : 0);
     }
     __syncwarp();
     fetch(t + kWarps * U);

@@ -83,7 +83,19 @@ __device__ __forceinline__ Vec32 ld_plain<Vec32>(const Vec32* p) {
   return r;
 }
 
-constexpr int kBwdGroup = 8;  // slots whose rows are in flight at once
+// Slots whose rows are in flight at once: 8, or 4 for single elements.
+template <typename V>
+__host__ __device__ constexpr int bwd_group() {
+  return sizeof(V) >= 16 ? 8 : 4;
+}
+
+// Vectors of a row in flight per thread and slot: one 16- or 32-byte vector,
+// four single elements (with one, the element path of 1999 tokens x 3 slots of
+// 1001 bf16 took 23.6 us, a chain of load latencies).
+template <typename V>
+__host__ __device__ constexpr int bwd_unroll() {
+  return sizeof(V) >= 16 ? 1 : 4;
+}
 
 // E may be null (no dw wanted), dE may be null (frozen experts).
 template <typename V, bool BF16>
@@ -93,6 +105,8 @@ __global__ void __launch_bounds__(kRowThreads)
                             V* __restrict__ dE, float* __restrict__ dw, long nvec, int k) {
   using R = RowVec<V, BF16>;
   constexpr int NE = R::kElems;
+  constexpr int VU = bwd_unroll<V>();
+  constexpr int kBwdGroup = bwd_group<V>();
   constexpr int kWarps = kRowThreads / 32;
   __shared__ long row_s[kRowMaxK];
   __shared__ float w_s[kRowMaxK];
@@ -113,31 +127,41 @@ __global__ void __launch_bounds__(kRowThreads)
       row[u] = j0 + u < k ? row_s[j0 + u] : -1;
       dot[u] = 0.0f;
     }
-    for (long v = threadIdx.x; v < nvec; v += kRowThreads) {
-      const V gv = ld_stream(g + v);
-      V e[kBwdGroup];
-      if (E) {
+    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kRowThreads) {
+      V gv[VU], e[VU][kBwdGroup];
 #pragma unroll
-        for (int u = 0; u < kBwdGroup; ++u)
-          e[u] = row[u] >= 0 ? ld_stream(E + row[u] * nvec + v) : V{};
-      }
-      float gf[NE];
-      R::unpack(gv, gf);
-#pragma unroll
-      for (int u = 0; u < kBwdGroup; ++u) {
-        if (row[u] < 0) continue;
+      for (int i = 0; i < VU; ++i) {
+        const long v = v0 + i * kRowThreads;
+        const bool in = VU == 1 || v < nvec;
+        gv[i] = in ? ld_stream(g + v) : V{};
         if (E) {
-          float ef[NE];
-          R::unpack(e[u], ef);
 #pragma unroll
-          for (int i = 0; i < NE; ++i) dot[u] = fmaf(gf[i], ef[i], dot[u]);
+          for (int u = 0; u < kBwdGroup; ++u)
+            e[i][u] = in && row[u] >= 0 ? ld_stream(E + row[u] * nvec + v) : V{};
         }
-        if (dE) {
-          const float wj = w_s[j0 + u];
-          float o[NE];
+      }
 #pragma unroll
-          for (int i = 0; i < NE; ++i) o[i] = wj * gf[i];
-          st_stream(dE + row[u] * nvec + v, R::pack(o));
+      for (int i = 0; i < VU; ++i) {
+        const long v = v0 + i * kRowThreads;
+        if (VU > 1 && v >= nvec) break;
+        float gf[NE];
+        R::unpack(gv[i], gf);
+#pragma unroll
+        for (int u = 0; u < kBwdGroup; ++u) {
+          if (row[u] < 0) continue;
+          if (E) {
+            float ef[NE];
+            R::unpack(e[i][u], ef);
+#pragma unroll
+            for (int c = 0; c < NE; ++c) dot[u] = fmaf(gf[c], ef[c], dot[u]);
+          }
+          if (dE) {
+            const float wj = w_s[j0 + u];
+            float o[NE];
+#pragma unroll
+            for (int c = 0; c < NE; ++c) o[c] = wj * gf[c];
+            st_stream(dE + row[u] * nvec + v, R::pack(o));
+          }
         }
       }
     }
@@ -168,38 +192,55 @@ __global__ void __launch_bounds__(kRowThreads)
                            int k) {
   using R = RowVec<V, BF16>;
   constexpr int NE = R::kElems;
+  constexpr int VU = bwd_unroll<V>();
+  constexpr int kBwdGroup = bwd_group<V>();
   __shared__ long row_s[kRowMaxK];
   for (long t = blockIdx.x; t < T; t += gridDim.x) {
     if (threadIdx.x < k) row_s[threadIdx.x] = inv[t * k + threadIdx.x];
     __syncthreads();
-    for (long v = threadIdx.x; v < nvec; v += kRowThreads) {
-      V av{};
-      if (add) av = ld_plain(add + t * nvec + v);
-      float acc[NE];
+    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kRowThreads) {
+      V av[VU];
+      float acc[VU][NE];
 #pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < VU; ++i) {
+        const long v = v0 + i * kRowThreads;
+        av[i] = add && v < nvec ? ld_plain(add + t * nvec + v) : V{};
+#pragma unroll
+        for (int c = 0; c < NE; ++c) acc[i][c] = 0.0f;
+      }
       for (int j0 = 0; j0 < k; j0 += kBwdGroup) {
-        V e[kBwdGroup];
+        V e[VU][kBwdGroup];
 #pragma unroll
         for (int u = 0; u < kBwdGroup; ++u) {
           const long r = j0 + u < k ? row_s[j0 + u] : -1;
-          e[u] = r >= 0 ? ld_stream(dxs + r * nvec + v) : V{};
+#pragma unroll
+          for (int i = 0; i < VU; ++i) {
+            const long v = v0 + i * kRowThreads;
+            e[i][u] = r >= 0 && v < nvec ? ld_stream(dxs + r * nvec + v) : V{};
+          }
         }
 #pragma unroll
-        for (int u = 0; u < kBwdGroup; ++u) {  // V{} of a missing slot adds 0
-          float ef[NE];
-          R::unpack(e[u], ef);
+        for (int u = 0; u < kBwdGroup; ++u)  // V{} of a missing slot adds 0
 #pragma unroll
-          for (int i = 0; i < NE; ++i) acc[i] += ef[i];
+          for (int i = 0; i < VU; ++i) {
+            float ef[NE];
+            R::unpack(e[i][u], ef);
+#pragma unroll
+            for (int c = 0; c < NE; ++c) acc[i][c] += ef[c];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < VU; ++i) {
+        const long v = v0 + i * kRowThreads;
+        if (v >= nvec) break;
+        if (add) {
+          float af[NE];
+          R::unpack(av[i], af);
+#pragma unroll
+          for (int c = 0; c < NE; ++c) acc[i][c] += af[c];
         }
+        st_stream(dx + t * nvec + v, R::pack(acc[i]));
       }
-      if (add) {
-        float af[NE];
-        R::unpack(av, af);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] += af[i];
-      }
-      st_stream(dx + t * nvec + v, R::pack(acc));
     }
     __syncthreads();
   }
