@@ -1537,6 +1537,30 @@ int launch_dw_planes(const void* planes, const void* x, float* out, int T, int d
   return launch_planes<true, 1, false>(ma, mb, gemm_params(N_r, d, T, slices, nullptr, out), sms, s);
 }
 
+// Launch as a programmatic dependent of the previous kernel on the stream (the
+// kernel itself waits for that one's results with griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+               Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MR_ERR_CUDA;
+  }
+  return MR_OK;
+}
+
 struct DxArgs {
   const void* W;
   bool wb;
@@ -1561,17 +1585,11 @@ int launch_dx_slots(const DxArgs& a) {
           cudaSuccess ||
       per_sm < 1)
     return MR_ERR_CUDA;
-  // token ranges per column chunk: two waves of resident CTAs, at least 64
-  // tokens each (a CTA first loads N_r * CW weights)
-  const int chunks = (a.d + CW - 1) / CW;
-  const long slots = (long)a.sms * per_sm;
-  long split = std::max<long>(1, slots * 2 / chunks);
-  split = std::min<long>(split, (a.T + 63) / 64);
-  const int per_cta = (int)((a.T + split - 1) / split);
-  const unsigned gy = (unsigned)((a.T + per_cta - 1) / per_cta);
-  kern<<<dim3((unsigned)chunks, gy), mr::rb::kDxThreads, smem, a.s>>>(
-      a.W, a.wb, a.idx, a.slot, a.add, a.dx, a.T, a.d, a.N_r, a.k, per_cta);
-  return launch_status();
+  constexpr int kBlock = mr::rb::kDxThreads / 32 * mr::rb::kDxTokens;
+  const long units = (long)((a.T + kBlock - 1) / kBlock) * ((a.d + CW - 1) / CW);
+  const unsigned grid = (unsigned)std::min<long>(units, (long)a.sms * per_sm);
+  return launch_pdl(kern, dim3(grid), dim3(mr::rb::kDxThreads), smem, a.s, a.W, a.wb, a.idx,
+                    a.slot, a.add, a.dx, a.T, a.d, a.N_r, a.k);
 }
 
 template <int CPL, bool VEC, bool BF16>
@@ -1582,7 +1600,8 @@ int launch_dx_k(const DxArgs& a) {
 
 template <bool BF16>
 int launch_dx(const DxArgs& a) {
-  const bool vec = a.d % 4 == 0 && aligned16(a.dx) && (!a.add || aligned16(a.add));
+  const bool vec = a.d % 4 == 0 && aligned16(a.dx) && (!a.add || aligned16(a.add)) &&
+                   (a.wb || aligned16(a.W));
   // 128 columns of every expert when they fit shared memory (N_r <= 419 at k = 8), else 64
   if (mr::rb::dx_smem_bytes(a.N_r, 128, a.k) <= 232448)
     return vec ? launch_dx_k<4, true, BF16>(a) : launch_dx_k<4, false, BF16>(a);
@@ -1591,12 +1610,13 @@ int launch_dx(const DxArgs& a) {
 
 template <typename V, bool BF16>
 int launch_dw_slots(const void* x, const int32_t* perm, const int32_t* offsets, const float* slot,
-                    int n, int N_r, int k, long nvec, float* dW, float* part, cudaStream_t s) {
+                    int n, int N_r, int k, long nvec, float* dW, float* part, bool after_dx,
+                    cudaStream_t s) {
   const unsigned pieces = (unsigned)((n + mr::rb::kDwRows - 1) / mr::rb::kDwRows + N_r);
   const unsigned slabs = (unsigned)((nvec + mr::rb::kDwThreads - 1) / mr::rb::kDwThreads);
-  mr::rb::dw_slots_kernel<V, BF16><<<dim3(pieces, slabs), mr::rb::kDwThreads, 0, s>>>(
-      static_cast<const V*>(x), perm, offsets, slot, n, N_r, k, nvec, dW, part);
-  return launch_status();
+  return launch_pdl(mr::rb::dw_slots_kernel<V, BF16>, dim3(pieces, slabs),
+                    dim3(mr::rb::kDwThreads), 0, s, static_cast<const V*>(x), perm, offsets, slot,
+                    n, N_r, k, nvec, dW, part, !after_dx);
 }
 
 // C = A . B on the CUDA cores (mr::rb::dense_kernel).
@@ -1758,12 +1778,13 @@ int mr_router_backward(const void* x, int x_dtype, const void* W, int W_dtype,
     const int n = T * k;
     const bool vec = aligned16(x) && d % (xb ? 8 : 4) == 0;
     if (vec)
-      rc = xb ? launch_dw_slots<uint4, true>(x, perm, offsets, slot, n, N_r, k, d / 8, dW, part, s)
-              : launch_dw_slots<uint4, false>(x, perm, offsets, slot, n, N_r, k, d / 4, dW, part, s);
+      rc = xb ? launch_dw_slots<uint4, true>(x, perm, offsets, slot, n, N_r, k, d / 8, dW, part, dx != nullptr, s)
+              : launch_dw_slots<uint4, false>(x, perm, offsets, slot, n, N_r, k, d / 4, dW, part, dx != nullptr, s);
     else
-      rc = xb ? launch_dw_slots<uint16_t, true>(x, perm, offsets, slot, n, N_r, k, d, dW, part, s)
-              : launch_dw_slots<float, false>(x, perm, offsets, slot, n, N_r, k, d, dW, part, s);
-    if (rc != MR_OK) return rc;
+      rc = xb ? launch_dw_slots<uint16_t, true>(x, perm, offsets, slot, n, N_r, k, d, dW, part, dx != nullptr, s)
+              : launch_dw_slots<float, false>(x, perm, offsets, slot, n, N_r, k, d, dW, part, dx != nullptr, s);
+    // no segment of more than kDwRows rows: nothing to join
+    if (rc != MR_OK || n <= mr::rb::kDwRows) return rc;
     mr::rb::dw_join_kernel<<<dim3((unsigned)N_r, (unsigned)((d + 1023) / 1024)), 256, 0, s>>>(
         offsets, n, N_r, d, part, dW);
     return launch_status();

@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kc = k0; kc < k1; ++kc, (++s == STAGES ? (s = 0, ph ^= 1u) : 0u)) {
           const bool first = (kc - k0) % kInterval == 0;
           const int buf = (int)(j & 1);
-          if (first && j >= 2 && !mbar_wait(bar(B_ACCE + buf), (uint32_t)(((j >> 1) - 1) & 1), abort)) {
+          if (first && j >= 2 &&
+              !mbar_wait(bar(B_ACCE + buf), (uint32_t)(((j >> 1) - 1) & 1), abort)) {
             go = false;
             break;
           }
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int pb = 0; pb < NPB; ++pb) {
                 if (pa + pb > 2) continue;
                 const uint32_t ap = a + pa * (BM * kBK * 2);
-                const uint64_t da = DW ? make_desc_mn(ap + kk * 2048) : make_desc_sw64(ap + kk * 32);
+                const uint64_t da =
+                    DW ? make_desc_mn(ap + kk * 2048) : make_desc_sw64(ap + kk * 32);
                 const uint64_t db = make_desc_mn(b + pb * kPlaneBytes + kk * 2048);
                 mma_bf16(dt, da, db, idesc, (!first || kk > 0 || pa < 2) ? 1u : 0u);
               }

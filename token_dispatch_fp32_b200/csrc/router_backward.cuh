@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(32 * kDlWarps)
                    const float* __restrict__ g, int T, int N_r, int k, float scale, float eps,
                    float* __restrict__ slot, float* __restrict__ dense,
                    __nv_bfloat16* __restrict__ planes) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long t = (long)blockIdx.x * kDlWarps + warp;
   if (t >= T) return;
@@ -122,11 +123,22 @@ __global__ void __launch_bounds__(32 * kDlWarps)
 // tokens: each slot is one conflict-free read of its expert's CW columns and
 // CPL fused multiply-adds per lane.  The k * d reads of W per token then come
 // from shared memory (128 bytes a cycle and SM), which is what bounds the
-// kernel, instead of L2.  A warp takes kDxTokens tokens at a time (independent
+// kernel, instead of L2.  The grid is one wave: the (column chunk, block of
+// tokens) pairs are dealt out evenly, so a CTA loads its columns of W once or
+// twice.  A warp takes kDxTokens tokens at a time (independent
 // reads in flight) and stages their (row, dl) pairs in its own piece of shared
 // memory, the next tokens' already on their way (addv may be dxv: neither is
 // __restrict__).
-constexpr int kDxThreads = 768;
+//
+// The kernel is a programmatic dependent of dlogits_kernel: W is loaded while
+// that runs.  Measured on the full DeepSeek-V3 batch (16384 tokens, 256
+// experts, with add): 170-180 us with dlogits_kernel, against 118 us for the reads
+// of shared memory alone; 1024 threads of 64 registers 205 us (spills), one
+// token per warp at a time 435 us.  It lets dw_slots_kernel start as its CTAs
+// finish (345 us for the whole call against 356 us one after the other); making
+// room for both on an SM (80 registers a thread) gained nothing, the spills
+// cost what the overlap saved.
+constexpr int kDxThreads = 512;
 constexpr int kDxTokens = 4;
 // (row, dl) pairs per lane of a warp's tokens: one for k <= 8, else up to four
 constexpr int kDxSmall = (kDxTokens * 8 + 31) / 32, kDxLarge = kDxTokens * kMaxK / 32;
@@ -134,14 +146,15 @@ constexpr int dx_pairs_per_lane(int k) { return k <= 8 ? kDxSmall : kDxLarge; }
 
 __host__ __device__ constexpr size_t dx_smem_bytes(int N_r, int cw, int k) {
   // two buffers per warp of kDxTokens rows of pairs, each padded to an even count
-  return ((size_t)N_r + 1) * cw * 4 + (size_t)(kDxThreads / 32) * 2 * kDxTokens * ((k + 1) & ~1) * 8;
+  return ((size_t)N_r + 1) * cw * 4 +
+         (size_t)(kDxThreads / 32) * 2 * kDxTokens * ((k + 1) & ~1) * 8;
 }
 
 template <int CPL, bool VEC, bool BF16, int kRegs>
 __global__ void __launch_bounds__(kDxThreads)
     dx_slots_kernel(const void* __restrict__ Wv, bool wbf16, const int32_t* __restrict__ idx,
                     const float* __restrict__ slot, const void* addv, void* dxv, int T, int d,
-                    int N_r, int k, int tokens_per_cta) {
+                    int N_r, int k) {
   constexpr int CW = 32 * CPL;
   constexpr int U = kDxTokens;
   constexpr int kWarps = kDxThreads / 32;
@@ -150,10 +163,6 @@ __global__ void __launch_bounds__(kDxThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kp = (k + 1) & ~1;
   int2* pairs = reinterpret_cast<int2*>(sm + (N_r + 1) * CW) + warp * 2 * U * kp;  // [2][U][kp]
-  const int c0 = blockIdx.x * CW;
-  const long t_begin = (long)blockIdx.y * tokens_per_cta;
-  const long t_end = t_begin + tokens_per_cta < T ? t_begin + tokens_per_cta : T;
-
   // the pairs of tokens t .. t + U - 1: id and dl; pair i of a lane belongs to
   // token tk[i] (U for none) and goes to place at[i] of the buffer
   int er[kRegs], tk[kRegs], at[kRegs];
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kDxThreads)
     tk[r] = i < U * k ? i / k : U;
     at[r] = tk[r] * kp + i % k;
   }
-  auto fetch = [&](long t) {
+  auto fetch = [&](long t, long t_end) {
 #pragma unroll
     for (int r = 0; r < kRegs; ++r) {
       const bool in = tk[r] < U && t + tk[r] < t_end;
@@ -172,120 +181,151 @@ __global__ void __launch_bounds__(kDxThreads)
       gr[r] = in ? slot[t * k + lane + 32 * r] : 0.0f;
     }
   };
-  long t = t_begin + warp * U;
-  fetch(t);
   for (int i = lane; i < 2 * U * kp; i += 32) pairs[i] = make_int2(N_r * CW, 0);  // odd k: padding
-  for (int i = threadIdx.x; i < (N_r + 1) * CW; i += kDxThreads) {
-    const int e = i / CW, c = c0 + i % CW;
-    float v = 0.0f;
-    if (e < N_r && c < d) {
-      v = wbf16 ? mr_bf16_to_f32(static_cast<const uint16_t*>(Wv)[(long)e * d + c])
-                : static_cast<const float*>(Wv)[(long)e * d + c];
-    }
-    Ws[i] = v;
-  }
-  __syncthreads();
   // columns of this lane: CPL consecutive ones (VEC) or every 32nd
   auto col = [&](int i) { return VEC ? lane * CPL + i : lane + 32 * i; };
-  const bool mine = c0 + lane * CPL < d;  // VEC: d is a multiple of CPL
-  for (int par = 0; t < t_end; t += kWarps * U, par ^= 1) {
-    int2* buf = pairs + par * U * kp;
-#pragma unroll
-    for (int r = 0; r < kRegs; ++r) {
-      const bool ok = er[r] >= 0 && er[r] < N_r;
-      if (tk[r] < U)
-        buf[at[r]] = make_int2((ok ? er[r] : N_r) * CW, ok ? __float_as_int(gr[r]) : 0);
-    }
-    __syncwarp();
-    fetch(t + kWarps * U);
-    float acc[U][CPL];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) acc[u][i] = 0.0f;
-    // add, on its way while the slots are summed
-    uint32_t ab[U][CPL / 2];
-    float af[U][CPL];
-    if (VEC && addv) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (t + u >= t_end || !mine) continue;
-        const long o = (t + u) * d + c0 + lane * CPL;
-        if constexpr (BF16) {
-          const uint16_t* a = static_cast<const uint16_t*>(addv) + o;
-          if constexpr (CPL == 4)
-            *reinterpret_cast<uint2*>(ab[u]) = *reinterpret_cast<const uint2*>(a);
-          else ab[u][0] = *reinterpret_cast<const uint32_t*>(a);
-        } else {
-          const float* a = static_cast<const float*>(addv) + o;
-          if constexpr (CPL == 4)
-            *reinterpret_cast<float4*>(af[u]) = *reinterpret_cast<const float4*>(a);
-          else *reinterpret_cast<float2*>(af[u]) = *reinterpret_cast<const float2*>(a);
-        }
-      }
-    }
+  constexpr int kBlock = kWarps * U;  // tokens per step of the CTA
+  const long blocks = ((long)T + kBlock - 1) / kBlock;
+  const long units = blocks * ((d + CW - 1) / CW);
+  const long u_end = units * (blockIdx.x + 1) / gridDim.x;
+  bool waited = false;
+  for (long unit = units * blockIdx.x / gridDim.x; unit < u_end;) {
+    const int c0 = (int)(unit / blocks) * CW;
+    const long b0 = unit % blocks;
+    const long b1 = b0 + (u_end - unit) < blocks ? b0 + (u_end - unit) : blocks;
+    unit += b1 - b0;
+    const long t_end = b1 * kBlock < T ? b1 * kBlock : T;
+    __syncthreads();  // the last chunk's columns have been read
+    if (VEC && !wbf16) {  // d is a multiple of 4, W 16-byte aligned
+      constexpr int Q = CW / 4;
 #pragma unroll 4
-    for (int j = 0; j < kp; j += 2) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int4 pr = *reinterpret_cast<const int4*>(buf + u * kp + j);
-        const float a0 = __int_as_float(pr.y), a1 = __int_as_float(pr.w);
-        const float *w0 = Ws + pr.x, *w1 = Ws + pr.z;
-        if constexpr (VEC && CPL == 4) {
-          const float4 v0 = *reinterpret_cast<const float4*>(w0 + lane * 4);
-          const float4 v1 = *reinterpret_cast<const float4*>(w1 + lane * 4);
-          acc[u][0] = fmaf(a1, v1.x, fmaf(a0, v0.x, acc[u][0]));
-          acc[u][1] = fmaf(a1, v1.y, fmaf(a0, v0.y, acc[u][1]));
-          acc[u][2] = fmaf(a1, v1.z, fmaf(a0, v0.z, acc[u][2]));
-          acc[u][3] = fmaf(a1, v1.w, fmaf(a0, v0.w, acc[u][3]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < CPL; ++i)
-            acc[u][i] = fmaf(a1, w1[col(i)], fmaf(a0, w0[col(i)], acc[u][i]));
-        }
+      for (int i = threadIdx.x; i < (N_r + 1) * Q; i += kDxThreads) {
+        const int e = i / Q, c = c0 + 4 * (i % Q);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < N_r && c < d)
+          v = __ldg(
+              reinterpret_cast<const float4*>(static_cast<const float*>(Wv) + (long)e * d + c));
+        *reinterpret_cast<float4*>(Ws + 4 * i) = v;
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < (N_r + 1) * CW; i += kDxThreads) {
+        const int e = i / CW, c = c0 + i % CW;
+        float v = 0.0f;
+        if (e < N_r && c < d)
+          v = wbf16 ? mr_bf16_to_f32(static_cast<const uint16_t*>(Wv)[(long)e * d + c])
+                    : static_cast<const float*>(Wv)[(long)e * d + c];
+        Ws[i] = v;
       }
     }
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // dlogits_kernel's slots
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      waited = true;
+    }
+    __syncthreads();
+    long t = b0 * kBlock + warp * U;
+    fetch(t, t_end);
+    const bool mine = c0 + lane * CPL < d;  // VEC: d is a multiple of CPL
+    for (int par = 0; t < t_end; t += kWarps * U, par ^= 1) {
+      int2* buf = pairs + par * U * kp;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u >= t_end) break;
-      const long base = (t + u) * d + c0;
-      if constexpr (VEC) {
-        if (!mine) continue;
-        if constexpr (BF16) {
-          uint32_t o[CPL / 2];
+      for (int r = 0; r < kRegs; ++r) {
+        const bool ok = er[r] >= 0 && er[r] < N_r;
+        if (tk[r] < U)
+          buf[at[r]] = make_int2((ok ? er[r] : N_r) * CW, ok ? __float_as_int(gr[r]) : 0);
+      }
+      __syncwarp();
+      fetch(t + kWarps * U, t_end);
+      float acc[U][CPL];
 #pragma unroll
-          for (int i = 0; i < CPL / 2; ++i) {
-            float lo = 0.0f, hi = 0.0f;
-            if (addv) bf16x2_unpack(ab[u][i], lo, hi);
-            o[i] = bf16x2_pack_rn(acc[u][2 * i] + lo, acc[u][2 * i + 1] + hi);
-          }
-          uint16_t* out = static_cast<uint16_t*>(dxv) + base + lane * CPL;
-          if constexpr (CPL == 4) __stcs(reinterpret_cast<uint2*>(out), make_uint2(o[0], o[1]));
-          else __stcs(reinterpret_cast<uint32_t*>(out), o[0]);
-        } else {
-          float* out = static_cast<float*>(dxv) + base + lane * CPL;
-          if (addv) {
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < CPL; ++i) acc[u][i] += af[u][i];
-          }
-          if constexpr (CPL == 4)
-            __stcs(reinterpret_cast<float4*>(out),
-                   make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]));
-          else __stcs(reinterpret_cast<float2*>(out), make_float2(acc[u][0], acc[u][1]));
-        }
-      } else {
+        for (int i = 0; i < CPL; ++i) acc[u][i] = 0.0f;
+      // add, on its way while the slots are summed
+      uint32_t ab[U][CPL / 2];
+      float af[U][CPL];
+      if (VEC && addv) {
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) {
-          const int c = col(i);
-          if (c0 + c >= d) continue;
-          float v = acc[u][i];
+        for (int u = 0; u < U; ++u) {
+          if (t + u >= t_end || !mine) continue;
+          const long o = (t + u) * d + c0 + lane * CPL;
           if constexpr (BF16) {
-            if (addv) v += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[base + c]);
-            const __nv_bfloat16 b = __float2bfloat16_rn(v);
-            static_cast<uint16_t*>(dxv)[base + c] = *reinterpret_cast<const uint16_t*>(&b);
+            const uint16_t* a = static_cast<const uint16_t*>(addv) + o;
+            if constexpr (CPL == 4)
+              *reinterpret_cast<uint2*>(ab[u]) = *reinterpret_cast<const uint2*>(a);
+            else ab[u][0] = *reinterpret_cast<const uint32_t*>(a);
           } else {
-            if (addv) v += static_cast<const float*>(addv)[base + c];
-            static_cast<float*>(dxv)[base + c] = v;
+            const float* a = static_cast<const float*>(addv) + o;
+            if constexpr (CPL == 4)
+              *reinterpret_cast<float4*>(af[u]) = *reinterpret_cast<const float4*>(a);
+            else *reinterpret_cast<float2*>(af[u]) = *reinterpret_cast<const float2*>(a);
+          }
+        }
+      }
+#pragma unroll 4
+      for (int j = 0; j < kp; j += 2) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int4 pr = *reinterpret_cast<const int4*>(buf + u * kp + j);
+          const float a0 = __int_as_float(pr.y), a1 = __int_as_float(pr.w);
+          const float *w0 = Ws + pr.x, *w1 = Ws + pr.z;
+          if constexpr (VEC && CPL == 4) {
+            const float4 v0 = *reinterpret_cast<const float4*>(w0 + lane * 4);
+            const float4 v1 = *reinterpret_cast<const float4*>(w1 + lane * 4);
+            acc[u][0] = fmaf(a1, v1.x, fmaf(a0, v0.x, acc[u][0]));
+            acc[u][1] = fmaf(a1, v1.y, fmaf(a0, v0.y, acc[u][1]));
+            acc[u][2] = fmaf(a1, v1.z, fmaf(a0, v0.z, acc[u][2]));
+            acc[u][3] = fmaf(a1, v1.w, fmaf(a0, v0.w, acc[u][3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i)
+              acc[u][i] = fmaf(a1, w1[col(i)], fmaf(a0, w0[col(i)], acc[u][i]));
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= t_end) break;
+        const long base = (t + u) * d + c0;
+        if constexpr (VEC) {
+          if (!mine) continue;
+          if constexpr (BF16) {
+            uint32_t o[CPL / 2];
+#pragma unroll
+            for (int i = 0; i < CPL / 2; ++i) {
+              float lo = 0.0f, hi = 0.0f;
+              if (addv) bf16x2_unpack(ab[u][i], lo, hi);
+              o[i] = bf16x2_pack_rn(acc[u][2 * i] + lo, acc[u][2 * i + 1] + hi);
+            }
+            uint16_t* out = static_cast<uint16_t*>(dxv) + base + lane * CPL;
+            if constexpr (CPL == 4) __stcs(reinterpret_cast<uint2*>(out), make_uint2(o[0], o[1]));
+            else __stcs(reinterpret_cast<uint32_t*>(out), o[0]);
+          } else {
+            float* out = static_cast<float*>(dxv) + base + lane * CPL;
+            if (addv) {
+#pragma unroll
+              for (int i = 0; i < CPL; ++i) acc[u][i] += af[u][i];
+            }
+            if constexpr (CPL == 4)
+              __stcs(reinterpret_cast<float4*>(out),
+                     make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]));
+            else __stcs(reinterpret_cast<float2*>(out), make_float2(acc[u][0], acc[u][1]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) {
+            const int c = col(i);
+            if (c0 + c >= d) continue;
+            float v = acc[u][i];
+            if constexpr (BF16) {
+              if (addv) v += mr_bf16_to_f32(static_cast<const uint16_t*>(addv)[base + c]);
+              const __nv_bfloat16 b = __float2bfloat16_rn(v);
+              static_cast<uint16_t*>(dxv)[base + c] = *reinterpret_cast<const uint16_t*>(&b);
+            } else {
+              if (addv) v += static_cast<const float*>(addv)[base + c];
+              static_cast<float*>(dxv)[base + c] = v;
+            }
           }
         }
       }
@@ -295,9 +335,10 @@ __global__ void __launch_bounds__(kDxThreads)
 
 // ---- sigmoid: dW[e] = sum over the sorted rows r of e of dl[perm[r]] * x[perm[r]/k]
 //
-// Each expert's segment is cut into pieces of kDwRows sorted rows; a CTA takes
-// one piece and one slab of columns (consecutive CTAs share the slab, so its
-// columns of x stay in L2 while every expert reads them).  An expert's first
+// Each expert's segment is cut into pieces of kDwRows sorted rows (at least
+// one, so that an expert without rows gets its zeros); a CTA takes one piece
+// and one slab of columns (consecutive CTAs share the slab, so its columns of x
+// stay in L2 while every expert reads them).  An expert's first
 // piece goes to dW, the others to `part`, and dw_join_kernel adds them in
 // order: no atomics, a long segment is spread over many SMs.
 constexpr int kDwRows = 256;
@@ -308,6 +349,10 @@ constexpr int kDwThreads = 128;
 struct Piece {
   int e, row0, rows, extra;  // extra: index in `part`, -1 for an expert's first piece
 };
+
+__device__ __forceinline__ int pieces(int rows) {
+  return rows > kDwRows ? (rows + kDwRows - 1) / kDwRows : 1;
+}
 
 // Finds piece `b` (all threads of the CTA call it; e = -1 past the last one).
 __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets, int N_r, int n,
@@ -327,9 +372,9 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
   int mine = 0, extra = 0;
   for (int e = e0; e < e1; ++e) {
     int lo;
-    const int p = (rows_of(e, lo) + kDwRows - 1) / kDwRows;
+    const int p = pieces(rows_of(e, lo));
     mine += p;
-    extra += p > 1 ? p - 1 : 0;
+    extra += p - 1;
   }
   int a = mine, x = extra;
 #pragma unroll
@@ -354,7 +399,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
   if (b >= before && b < before + mine) {
     for (int e = e0; e < e1; ++e) {
       int lo;
-      const int cnt = rows_of(e, lo), p = (cnt + kDwRows - 1) / kDwRows;
+      const int cnt = rows_of(e, lo), p = pieces(cnt);
       if (b < before + p) {
         const int i = b - before;
         found.e = e;
@@ -364,7 +409,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
         break;
       }
       before += p;
-      xb += p > 1 ? p - 1 : 0;
+      xb += p - 1;
     }
   }
   __syncthreads();
@@ -376,12 +421,21 @@ template <typename V, bool BF16>
 __global__ void __launch_bounds__(kDwThreads)
     dw_slots_kernel(const V* __restrict__ x, const int32_t* __restrict__ perm,
                     const int32_t* __restrict__ offsets, const float* __restrict__ slot, int n,
-                    int N_r, int k, long nvec, float* __restrict__ dW, float* __restrict__ part) {
+                    int N_r, int k, long nvec, float* __restrict__ dW, float* __restrict__ part,
+                    bool wait_first) {
   using R = RowVec<V, BF16>;
   constexpr int NE = R::kElems;
   constexpr int U = 8;
+  // Programmatic dependent of dlogits_kernel (wait_first), or of dx_slots_kernel,
+  // every CTA of which (one wave) has seen dlogits_kernel complete before this
+  // kernel starts; then only this kernel's end waits for that one's, so that
+  // whatever follows on the stream comes after both.
+  if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
   const Piece pc = find_piece(offsets, N_r, n, blockIdx.x);
-  if (pc.e < 0) return;
+  if (pc.e < 0) {
+    if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   __shared__ int tok[kDwRows];
   __shared__ float gs[kDwRows];
   for (int i = threadIdx.x; i < pc.rows; i += kDwThreads) {
@@ -393,33 +447,35 @@ __global__ void __launch_bounds__(kDwThreads)
   }
   __syncthreads();
   const long v = (long)blockIdx.y * kDwThreads + threadIdx.x;
-  if (v >= nvec) return;
-  float acc[NE];
+  if (v < nvec) {
+    float acc[NE];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-  for (int r = 0; r < pc.rows; r += U) {
-    V xv[U];
+    for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+    for (int r = 0; r < pc.rows; r += U) {
+      V xv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = r + u < pc.rows ? tok[r + u] : -1;
-      xv[u] = t >= 0 ? ld_stream(x + (long)t * nvec + v) : V{};
+      for (int u = 0; u < U; ++u) {
+        const int t = r + u < pc.rows ? tok[r + u] : -1;
+        xv[u] = t >= 0 ? ld_stream(x + (long)t * nvec + v) : V{};
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float g = r + u < pc.rows ? gs[r + u] : 0.0f;
+        float xf[NE];
+        R::unpack(xv[u], xf);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) acc[i] = fmaf(g, xf[i], acc[i]);
+      }
     }
+    const long d = nvec * NE;
+    float* out = (pc.extra < 0 ? dW + (long)pc.e * d : part + (long)pc.extra * d) + v * NE;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float g = r + u < pc.rows ? gs[r + u] : 0.0f;
-      float xf[NE];
-      R::unpack(xv[u], xf);
-#pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] = fmaf(g, xf[i], acc[i]);
-    }
+    for (int i = 0; i < NE; ++i) out[i] = acc[i];
   }
-  const long d = nvec * NE;
-  float* out = (pc.extra < 0 ? dW + (long)pc.e * d : part + (long)pc.extra * d) + v * NE;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) out[i] = acc[i];
+  if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// dW[e] += the extra pieces of e, in order; 0 for an expert without rows.
+// dW[e] += the extra pieces of e, in order.
 __global__ void __launch_bounds__(256)
     dw_join_kernel(const int32_t* __restrict__ offsets, int n, int N_r, int d,
                    const float* __restrict__ part, float* __restrict__ dW) {
@@ -431,9 +487,9 @@ __global__ void __launch_bounds__(256)
       int lo = offsets[i], hi = offsets[i + 1];
       lo = lo < 0 ? 0 : lo;
       hi = hi > n ? n : hi;
-      const int p = hi > lo ? (hi - lo + kDwRows - 1) / kDwRows : 0;
+      const int p = pieces(hi - lo);
       if (i == e) mine = p;
-      else x += p > 1 ? p - 1 : 0;
+      else x += p - 1;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -447,9 +503,9 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int first = first_s, count = count_s;
-  if (count == 1) return;
+  if (count <= 1) return;
   for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < d; c += gridDim.y * blockDim.x) {
-    float s = count ? dW[(long)e * d + c] : 0.0f;
+    float s = dW[(long)e * d + c];
     for (int i = 0; i + 1 < count; ++i) s += part[(long)(first + i) * d + c];
     dW[(long)e * d + c] = s;
   }
