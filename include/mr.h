@@ -613,7 +613,8 @@ int mr_combine(const void *expert_out, int dtype, const float *w,
  *   w, inv_perm  as mr_combine.
  *   dexpert    [T*k, d] of `dtype`, or NULL: row inv_perm[t*k+j] gets
  *              w[t,j] * dy[t], rounded once.  Rows that no slot names (those
- *              of dropped slots) are not written.
+ *              of dropped slots) are not written.  An entry of inv_perm past
+ *              the T*k rows counts as dropped and raises the device flag.
  *   dw         [T, k] fp32, or NULL: dw[t,j] = sum_c dy[t,c] *
  *              expert_out[inv_perm[t*k+j]][c] in fp32; 0 for a dropped slot.
  * One kernel, no atomics: the results do not change from run to run.
@@ -629,7 +630,8 @@ int mr_combine_backward(const void *dy, int dtype, const void *expert_out,
  * gradients of its k sorted rows.
  *
  *   dxs       [T*k, d] gradients of the sorted rows, `dtype` MR_BF16 or MR_F32.
- *   inv_perm  [T*k] from mr_dispatch; a slot whose entry is -1 adds nothing.
+ *   inv_perm  [T*k] from mr_dispatch; a slot whose entry is -1 adds nothing (nor
+ *             does one past the T*k rows, which raises the device flag).
  *   add       [T, d] of `dtype` added to the sum (the gradient of x's other
  *             uses, e.g. the shared expert), or NULL.  May be dx itself.
  *   dx        [T, d] of `dtype`: dx[t] = sum_j dxs[inv_perm[t*k+j]] + add[t],
@@ -709,7 +711,8 @@ int mr_router_backward(const void *x, int x_dtype, const void *W, int W_dtype,
  * better served by mr_expert_gemm_gather.
  * mr_expert_w4_packed_bytes returns 0 for arguments it does not know.
  * Limits: group 32, 64 or 128, d % 8 == 0, N_r <= 1024, N_r * n_out < 2^31,
- * 16-byte aligned x (else MR_ERR_UNSUPPORTED).
+ * T*k <= 2^24, 16-byte aligned x (else MR_ERR_UNSUPPORTED).  An entry of perm
+ * outside [0, T*k) inside a segment raises the device flag (MR_ERR_DEVICE).
  */
 size_t mr_expert_w4_packed_bytes(int N_r, int n_out, int d, int group,
                                  int scale_dtype);

@@ -37,13 +37,14 @@
 // value 0 (nibble 8) and scale 0.
 //
 // The kernel is persistent, two CTAs per SM.  An item is 64 output rows of one
-// expert against up to `xr` of its sorted rows; the CTA's eight warps split
-// the columns (warp w takes units w, w + 8, ..) and meet in shared memory at
-// the item's end, adding in warp order.  Each warp has its own ring of units
+// expert against up to `xr` of its sorted rows; a team of `ks` of the CTA's
+// eight warps (chosen from the number of items) takes it, splits its columns (member m takes units m, m + ks, ..)
+// and meets in shared memory at the item's end, adding in member order.  Each
+// warp has its own ring of units
 // in shared memory, filled by one bulk copy each, and requests a unit as soon
 // as it has finished the one whose place it takes, through the ends of items,
-// so that the stream from HBM does not pause; no warp waits for another but at
-// an item's end.  x comes through L1.  Every mbarrier wait is bounded.
+// so that the stream from HBM does not pause; no warp waits for another but its
+// team at an item's end.  x comes through L1.  Every mbarrier wait is bounded.
 #pragma once
 
 #include <type_traits>
@@ -308,17 +309,38 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
   __syncthreads();
   const long items = (long)sh.first[P.N_r] * P.tiles;
 
+  // Team size: a team spends about KB / ks units and two units' time of its own
+  // (finding the item, the rows' first loads, the meeting) on each item, and
+  // half an item is lost at the end.  Measured, ks = 8 / 4 / 2 / 1: decode batch
+  // of 64 tokens (256 experts, d = 7168, 7104 items) 441 / 412 / 398 / 397 us,
+  // 8 tokens (1820 items) 129 / 118 / 134 / 131 us, one token (256 items) 26 /
+  // 27 / 45 / 81 us, 200 tokens on 8 experts (d = 1408, 2640 items) 88 / 71 / 66
+  // / 72 us.
+  int ks = kWarps;
+  float best = INFINITY;
+  for (int c = kWarps; c >= 1; c /= 2) {
+    const float item_cost = (float)((P.KB + c - 1) / c + 2);
+    const float cost = ((float)items / (float)(gridDim.x * (kWarps / c)) + 0.5f) * item_cost;
+    if (cost < best) {
+      best = cost;
+      ks = c;
+    }
+  }
+  const int team = warp / ks, member = warp % ks;
+  const long stride = (long)gridDim.x * (kWarps / ks);
+  const long item0 = (long)blockIdx.x * (kWarps / ks) + team;
+
   // ---- the warp's ring ---------------------------------------------------------
   uint8_t* slots = ring + warp * kStages * P.unit_bytes;
   Walk ahead;  // the next unit to request
-  ahead.item = warp < P.KB ? (long)blockIdx.x : items;
-  ahead.kb = warp;
+  ahead.item = member < P.KB ? item0 : items;
+  ahead.kb = member;
   const uint8_t* src = nullptr;
-  const long stride = (long)kWarps * P.unit_bytes;
+  const long step_bytes = (long)ks * P.unit_bytes;
   auto start = [&]() {
     if (ahead.item >= items) return;
     find(P, sh, ahead);
-    src = P.wp + (((long)ahead.e * P.tiles + ahead.tile) * P.KB + warp) * (long)P.unit_bytes;
+    src = P.wp + (((long)ahead.e * P.tiles + ahead.tile) * P.KB + member) * (long)P.unit_bytes;
   };
   start();
   int requested = 0, used = 0;
@@ -331,11 +353,11 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
       eg::bulk_load(smem_u32(slots + s * P.unit_bytes), src, (uint32_t)P.unit_bytes, bar);
     }
     ++requested;
-    ahead.kb += kWarps;
-    src += stride;
+    ahead.kb += ks;
+    src += step_bytes;
     if (ahead.kb >= P.KB) {
-      ahead.kb = warp;
-      ahead.item += gridDim.x;
+      ahead.kb = member;
+      ahead.item += stride;
       start();
     }
   };
@@ -358,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
         if (p < 0 || p >= n) mr_raise(MR_FLAG_BAD_INDEX);
       }
       x4[t] = reinterpret_cast<const uint4*>(P.x + (long)tok * P.d) + lane % 4 +
-              warp * (kCols / 8);
+              member * (kCols / 8);
     }
     float acc[4][NT][4];
 #pragma unroll
@@ -371,9 +393,9 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
     if constexpr (NT == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        load_x<NT>(x4, i, warp < P.KB ? P.d / 8 - warp * (kCols / 8) : 0, lane, xn[i]);
+        load_x<NT>(x4, i, member < P.KB ? P.d / 8 - member * (kCols / 8) : 0, lane, xn[i]);
     }
-    for (int kb = warp; kb < P.KB; kb += kWarps) {
+    for (int kb = member; kb < P.KB; kb += ks) {
       const int s = used % kStages, n8 = P.d / 8 - kb * (kCols / 8);
       const uint8_t* w = slots + s * P.unit_bytes;
       const uint32_t bar = smem_u32(&sh.bars[warp][s]), ph = (uint32_t)(used / kStages) & 1u;
@@ -381,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
         uint4 xc[4][NT];
 #pragma unroll
         for (int i = 0; i < 4; ++i) xc[i][0] = xn[i][0];
-        if (kb + kWarps < P.KB) {
-          x4[0] += kWarps * (kCols / 8);
+        if (kb + ks < P.KB) {
+          x4[0] += ks * (kCols / 8);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load_x<NT>(x4, i, n8 - kWarps * (kCols / 8), lane, xn[i]);
+          for (int i = 0; i < 4; ++i) load_x<NT>(x4, i, n8 - ks * (kCols / 8), lane, xn[i]);
         }
         go = go && __all_sync(0xffffffffu, mbar_wait(bar, ph, abort));
         if (!go) break;
@@ -405,10 +427,10 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
       if constexpr (NT > 1) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          x4[t] += kWarps * (kCols / 8);
+          x4[t] += ks * (kCols / 8);
       }
     }
-    // the warps' sums meet, one tile of 8 rows of x at a time: acc 0, 1 are rows
+    // the team's sums meet, one tile of 8 rows of x at a time: acc 0, 1 are rows
     // 2 (lane % 4), + 1 of x against output row 16 m + lane / 4; acc 2, 3 the
     // same against 16 m + 8 + lane / 4
 #pragma unroll
@@ -420,14 +442,13 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine[4 * m + i] = acc[m][t][i];
-      __syncthreads();
-      for (int o = tid; o < 8 * kTile; o += kThreads) {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * ks) : "memory");
+      for (int o = member * 32 + lane; o < 8 * kTile; o += 32 * ks) {
         const int c = o / kTile, r = o % kTile;
-        const float* src = red + ((r % 8) * 4 + c / 2) * kRedLane + 4 * (r / 16) + (c & 1) +
+        const float* src = red + team * ks * 32 * kRedLane + ((r % 8) * 4 + c / 2) * kRedLane + 4 * (r / 16) + (c & 1) +
                            2 * ((r / 8) & 1);
         float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += src[w * 32 * kRedLane];
+        for (int w = 0; w < ks; ++w) v += src[w * 32 * kRedLane];
         const int row = t * 8 + c, col = k.tile * kTile + r;
         if (row < k.rows && col < P.n_out && !*abort) {
           const __nv_bfloat16 b = __float2bfloat16_rn(v);
@@ -436,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
       }
     }
   };
-  for (long it = blockIdx.x; it < items; it += gridDim.x) {
+  for (long it = item0; it < items; it += stride) {
     Walk k;
     k.item = it;
     find(P, sh, k);

@@ -1856,6 +1856,7 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   if (T < 0 || k <= 0 || (long long)T * k >= (1LL << 31)) return MR_ERR_INVALID_ARG;
   const int rc = check_w4(N_r, n_out, d, group, scale_dtype);
   if (rc != MR_OK) return rc;
+  if ((long long)T * k > (1LL << 24)) return MR_ERR_UNSUPPORTED;  // the passes are counted in 32 bits
   if (T == 0) return MR_OK;
   if (!x || !offsets || !packed || !out) return MR_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(packed)) return MR_ERR_UNSUPPORTED;

@@ -406,6 +406,11 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
         found.row0 = lo + i * kDwRows;
         found.rows = cnt - i * kDwRows < kDwRows ? cnt - i * kDwRows : kDwRows;
         found.extra = i == 0 ? -1 : xb + i - 1;
+        // more extra pieces than `part` holds: offsets that overlap
+        if (found.extra >= n / kDwRows) {
+          found.e = -1;
+          mr_raise(MR_FLAG_BAD_INDEX);
+        }
         break;
       }
       before += p;
@@ -503,7 +508,7 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int first = first_s, count = count_s;
-  if (count <= 1) return;
+  if (count <= 1 || first + count - 1 > n / kDwRows) return;
   for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < d; c += gridDim.y * blockDim.x) {
     float s = dW[(long)e * d + c];
     for (int i = 0; i + 1 < count; ++i) s += part[(long)(first + i) * d + c];

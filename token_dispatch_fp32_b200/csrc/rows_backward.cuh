@@ -97,6 +97,14 @@ __host__ __device__ constexpr int bwd_unroll() {
   return sizeof(V) >= 16 ? 1 : 4;
 }
 
+// Sorted row of slot i of T * k, -1 for none: a dropped slot, or (flagged) an
+// entry past the rows.
+__device__ __forceinline__ long slot_row(const int32_t* inv, long i, long rows) {
+  const long r = inv[i];
+  if (r >= rows) mr_raise(MR_FLAG_BAD_INDEX);
+  return r >= 0 && r < rows ? r : -1;
+}
+
 // E may be null (no dw wanted), dE may be null (frozen experts).
 template <typename V, bool BF16>
 __global__ void __launch_bounds__(kRowThreads)
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const long t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < k) {
-    row_s[threadIdx.x] = inv[t * k + threadIdx.x];
+    row_s[threadIdx.x] = slot_row(inv, t * k + threadIdx.x, (long)gridDim.x * k);
     w_s[threadIdx.x] = w[t * k + threadIdx.x];
   }
   __syncthreads();
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int kBwdGroup = bwd_group<V>();
   __shared__ long row_s[kRowMaxK];
   for (long t = blockIdx.x; t < T; t += gridDim.x) {
-    if (threadIdx.x < k) row_s[threadIdx.x] = inv[t * k + threadIdx.x];
+    if (threadIdx.x < k) row_s[threadIdx.x] = slot_row(inv, t * k + threadIdx.x, T * k);
     __syncthreads();
     for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kRowThreads) {
       V av[VU];
