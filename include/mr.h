@@ -635,7 +635,8 @@ int mr_combine_backward(const void *dy, int dtype, const void *expert_out,
  *   add       [T, d] of `dtype` added to the sum (the gradient of x's other
  *             uses, e.g. the shared expert), or NULL.  May be dx itself.
  *   dx        [T, d] of `dtype`: dx[t] = sum_j dxs[inv_perm[t*k+j]] + add[t],
- *             summed in fp32 in slot order, rounded once.
+ *             summed in fp32 in slot order, rounded once.  Must not overlap
+ *             dxs.
  * One kernel, no atomics.  Limits: 1 <= k <= 32.
  */
 int mr_gather_rows_backward(const void *dxs, int dtype,
@@ -674,8 +675,13 @@ int mr_gather_rows_backward(const void *dxs, int dtype,
  *             (sigmoid) and for T == 0.
  *   workspace at least mr_router_backward_workspace_size(T, d, N_r, k, flags)
  *             bytes, 16-byte aligned; its contents need no initialisation.
- * All products and sums in fp32 (fp32-level accuracy), in a fixed order.
- * Calls that may overlap need different workspaces.
+ * The outputs must not overlap each other, the workspace or (but for add and
+ * dx) the inputs.  All products and sums have fp32-level accuracy and a fixed
+ * order: fp32 fused multiply-adds, or for softmax's dense products the sums of
+ * bf16 planes' products on the tensor cores (as the forward's bf16x3).  Entries
+ * of perm out of range inside a segment, or offsets that overlap, raise the
+ * device flag (MR_ERR_DEVICE).  Calls that may overlap need different
+ * workspaces.
  * Limits: N_r <= 512, 1 <= k <= 32; at least one of dlogits, dx and dW.
  */
 size_t mr_router_backward_workspace_size(int T, int d, int N_r, int k,

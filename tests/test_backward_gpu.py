@@ -164,6 +164,9 @@ GATE = [  # T, d, N_r, k, x, W, hot experts
     (1, 7168, 256, 8, "bf16", "f32", 0),     # one token
     (40, 128, 48, 32, "bf16", "f32", 0),     # k = 32
     (513, 64, 16, 1, "f32", "f32", 1),       # every token on one expert
+    (33, 67, 20, 3, "bf16", "bf16", 0),      # odd rows of both
+    (777, 264, 21, 3, "bf16", "f32", 0),     # experts no multiple of 8, a K tail of tokens
+    (1100, 520, 130, 8, "bf16", "bf16", 3),  # experts just past one tensor-core tile
 ]
 
 
@@ -247,6 +250,59 @@ def test_router_backward_extreme_logits(softmax):
     got = mr.mr_router_backward(_dev(x), _dev(W), _f32(L), _i32(idx), _f32(g), _i32(perm),
                                 _i32(offsets), 2.5, flags=flags, dlogits=dlog)
     _check_gate(x, W, L, idx, g, "f32", flags, None, (*got, dlog))
+
+
+@pytest.mark.parametrize("softmax", [False, True], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("xdt", ["bf16", "f32"])
+def test_router_backward_on_unaligned_buffers(softmax, xdt):
+    """x, W, add and dx 4 bytes past a 16-byte boundary: the element paths."""
+    T, d, N_r, k = 150, 256, 32, 4
+    rng, x, W, L, idx, g = _gate_problem(T, d, N_r, k, xdt, "f32", 0, seed=9)
+    add = _rows(rng, (T, d), xdt)
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    dlog = torch.empty((T, N_r), device="cuda")
+    flags = mr.MR_SCORE_SOFTMAX if softmax else 0
+    out = _offset_view(np.zeros_like(x), 4)
+    dx, dW = mr.mr_router_backward(_offset_view(x, 4), _offset_view(W, 4), _f32(L), _i32(idx),
+                                   _f32(g), _i32(perm), _i32(offsets), 2.5, flags=flags,
+                                   add=_offset_view(add, 4), dx=out,
+                                   dW=_offset_view(np.zeros_like(W), 4), dlogits=dlog)
+    assert mr.mr_get_error() == mr.MR_OK
+    _check_gate(x, W, L, idx, g, xdt, flags, add, (dx, dW, dlog))
+
+
+def test_router_backward_drops_a_bad_permutation():
+    """Entries of perm out of range, and offsets that overlap, do not reach
+    memory: they are flagged."""
+    T, d, N_r, k = 600, 64, 16, 2
+    _, x, W, L, idx, g = _gate_problem(T, d, N_r, k, "f32", "f32", 1, seed=2)
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    bad = perm.copy()
+    bad[[0, 700]] = T * k, -7
+    args = (_dev(x), _dev(W), _f32(L), _i32(idx), _f32(g))
+    mr.mr_router_backward(*args, _i32(bad), _i32(offsets), 2.5)
+    assert mr.mr_get_error() == mr.MR_ERR_DEVICE
+    over = np.where(np.arange(N_r + 1) % 2, T * k, 0)  # every second segment is everything
+    mr.mr_router_backward(*args, _i32(perm), _i32(over), 2.5)
+    assert mr.mr_get_error() == mr.MR_ERR_DEVICE
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_row_gradients_drop_entries_past_the_rows(dtype):
+    T, d, k, N_r = 40, 64, 2, 8
+    rng, inv, w, dy, E = _combine_problem(T, d, k, N_r, dtype, seed=3)
+    bad = inv.copy()
+    bad[7], bad[20] = T * k, 1 << 30
+    ref = np.where(np.isin(np.arange(T * k), [7, 20]), -1, inv)
+    got = mr.mr_combine_backward(_dev(dy), _dev(E), _f32(w), _i32(bad),
+                                 dexpert=_dev(np.zeros_like(E)))
+    assert mr.mr_get_error() == mr.MR_ERR_DEVICE
+    want = mr.mr_combine_backward(_dev(dy), _dev(E), _f32(w), _i32(ref),
+                                  dexpert=_dev(np.zeros_like(E)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = mr.mr_gather_rows_backward(_dev(E), k, _i32(bad))
+    assert mr.mr_get_error() == mr.MR_ERR_DEVICE
+    assert torch.equal(got, mr.mr_gather_rows_backward(_dev(E), k, _i32(ref)))
 
 
 def test_router_backward_without_tokens():

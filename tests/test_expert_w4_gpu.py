@@ -123,6 +123,25 @@ def test_expert_w4_keeps_rows_apart():
     assert not torch.isfinite(out[tok == 9]).any()
 
 
+@pytest.mark.parametrize("spread", [0, 12, 20, 60])
+def test_expert_w4_spread_magnitudes(spread):
+    """Rows whose values spread over `spread` binary orders of magnitude, rows
+    of very small and very large values and a row of zeros: the bound holds,
+    nothing overflows on the way."""
+    T, k, N_r, n_out, d = 8, 2, 4, 64, 512
+    x, perm, offsets, _, q, s = _problem(T, k, N_r, n_out, d, 32, "bf16", 6 + spread)
+    rng = np.random.default_rng(spread)
+    v = widen(x) * 2.0 ** rng.integers(-spread, 1, (T, d))
+    v[1] *= 2.0 ** -100
+    v[2] *= 2.0 ** 100
+    v[3] = 0
+    x = (v.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    W4 = mr.mr_expert_pack_w4(torch.from_numpy(q).cuda(), _dev(s), 32)
+    out = mr.mr_expert_gemv_gather_w4(_dev(x), k, _i32(perm), _i32(offsets), W4, N_r, n_out, 32)
+    want, mag, magx = gr.expert_w4(widen(x), perm, offsets, q, widen(s), 32, k)
+    gr.check(widen(_host(out)), want, _bound(d, mag, magx), "bf16", "out")
+
+
 @pytest.mark.parametrize("mode", ["eager", "graph"])
 def test_decode_step_of_a_moe_layer(mode):
     """Gate, dispatch, experts on 4-bit weights, combine for a few tokens;

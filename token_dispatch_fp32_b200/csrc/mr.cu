@@ -1882,7 +1882,10 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   const long n = (long)T * k;
   P.xr = mr::w4::kRowsPerPass;
   const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
-  const unsigned grid = (unsigned)std::min<long>(items, 2l * sms);
+  // two CTAs per SM where their rings fit (all but fp32 scales of 32 columns, or
+  // more than about 600 experts)
+  const long per_sm = mr::w4::smem_bytes(l.unit_bytes, N_r) <= 113 * 1024 ? 2 : 1;
+  const unsigned grid = (unsigned)std::min<long>(items, per_sm * sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (sb == 2) {
     if (group == 32) return launch_expert_w4<32, uint16_t>(P, grid, s);
