@@ -6,7 +6,10 @@ to it, u the nibble: four MMA steps, each exact in its products and rounding
 within 2 fp32 steps (2 * 2^-23) of its largest partial sum, which is at most
 (24 + 31) sum |x|; hence 4 * 2 * 55 = 440 * 2^-23 of the scaled sum of |x|.
 Groups and warps then add in fp32: at most (d / 128 + 16) * 2^-23 of the sum
-of the magnitudes.  Plus half a step of the bf16 output."""
+of the magnitudes.  Segments of more than 32 rows: the scaled weight is exact in
+two bf16 planes (fp32 scales: the fp32 product, off by 2^-24, in three), so each
+of the 3 d / 16 MMA steps at most rounds within 2 fp32 steps of the sum of the
+magnitudes: (3 d / 8 + 2) * 2^-23 of it.  Plus half a step of the bf16 output."""
 import numpy as np
 import pytest
 import torch
@@ -32,7 +35,9 @@ def _problem(T, k, N_r, n_out, d, group, sdt, seed, hot=0):
 
 
 def _bound(d, mag, magx):
-    return ((d / 128 + 16) * mag + 440 * magx) * 2.0 ** -23
+    few = (d / 128 + 16) * mag + 440 * magx
+    many = (3 * d / 8 + 2) * mag
+    return np.maximum(few, many) * 2.0 ** -23
 
 
 CASES = [  # T, k, N_r, n_out, d, group, scales, hot
@@ -45,6 +50,13 @@ CASES = [  # T, k, N_r, n_out, d, group, scales, hot
     (64, 2, 4, 40, 384, 32, "bf16", 2),      # 64 rows on each of two experts
     (100, 1, 3, 16, 2048, 128, "bf16", 1),   # 100 rows on one
     (37, 2, 128, 31, 72, 32, "bf16", 0),
+    # long segments, enough of them that the many-row kernel takes them
+    (1100, 1, 1, 1000, 136, 32, "f32", 0),   # six blocks of one expert, a K tail
+    (600, 4, 8, 456, 1096, 128, "bf16", 1),  # one longer than three blocks
+    (193, 8, 8, 2050, 64, 64, "bf16", 0),    # two blocks each, one stage of columns
+    (290, 4, 16, 1100, 200, 64, "f32", 3),   # short segments among long ones
+    (500, 8, 64, 256, 512, 32, "bf16", 0),   # every segment about 60 rows
+    (64, 8, 8, 2300, 72, 32, "bf16", 0),     # one block of 64 rows each
 ]
 
 
@@ -69,9 +81,9 @@ def test_expert_w4(T, k, N_r, n_out, d, group, sdt, hot):
 def test_expert_w4_exact_on_integers(group):
     """Integer rows and power-of-two scales: every sum is exact in fp32, so the
     result is the exact value rounded once (to nearest even)."""
-    T, k, N_r, n_out, d = 20, 2, 6, 70, 640
+    T, k, N_r, n_out, d = 500, 2, 6, 1900, 640
     rng = np.random.default_rng(group)
-    _, offsets, perm, _ = oracle.dispatch(_ids(rng, T, k, N_r), N_r)
+    _, offsets, perm, _ = oracle.dispatch(_ids(rng, T, k, N_r, hot=1), N_r)  # 500 rows on one
     x = rng.integers(-4, 5, (T, d)).astype(np.float32)
     q = rng.integers(0, 256, (N_r, n_out, d // 2)).astype(np.uint8)
     s = (2.0 ** rng.integers(-3, 3, (N_r, n_out, d // group))).astype(np.float32)
@@ -106,10 +118,11 @@ def test_expert_w4_leaves_other_rows():
     assert (out[n:] == 7.0).all()
 
 
-def test_expert_w4_keeps_rows_apart():
+@pytest.mark.parametrize("T,n_out", [(24, 32), (80, 3700)], ids=["few", "many"])
+def test_expert_w4_keeps_rows_apart(T, n_out):
     """A NaN or an infinity in one token's row reaches that token's outputs
     only."""
-    T, k, N_r, n_out, d = 24, 2, 4, 32, 384
+    k, N_r, d = 4, 4, 384
     x, perm, offsets, _, q, s = _problem(T, k, N_r, n_out, d, 32, "bf16", 5)
     W4 = mr.mr_expert_pack_w4(torch.from_numpy(q).cuda(), _dev(s), 32)
     args = (k, _i32(perm), _i32(offsets), W4, N_r, n_out, 32)

@@ -149,6 +149,8 @@ struct Params {
   const uint8_t* wp;
   uint16_t* out;
   int T, d, k, N_r, n_out, tiles, KB, unit_bytes, xr;
+  int tile_rows;  // segments of more rows may go to expert_w4_tile.cuh's kernel (0: never)
+  int sms;
 };
 
 // The scales of step i: s[2 m + h] for the row 16 m + 8 h + lane / 4.
@@ -226,12 +228,45 @@ __device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const ui
   }
 }
 
+// Whether the segments of more than kLongRows rows go to the many-row kernel
+// (expert_w4_tile.cuh), decided alike by both kernels from the segments:
+// `passes` passes of 16 of their rows here, or `blocks` blocks there.  There a
+// 128-row tile of n_out takes an SM 0.7 us for 64 columns, however few the
+// blocks; here a unit and pass takes the whole GPU about 1.4 ns.  Measured (d =
+// 7168, n_out = 2048), here / there: 1 x 128 rows 32 / 96 us, 8 x 48 rows 88 / 84,
+// 8 x 128 rows 150 / 99, 256 x 128 rows 3.7 / 2.9 ms.
+constexpr int kLongRows = 32;
+constexpr int kTileRows = 192;  // rows per block there
+__device__ __forceinline__ bool long_to_tile(long passes, long blocks, int n_out, int sms) {
+  const long items = blocks * ((n_out + 127) / 128);
+  return passes * ((n_out + kTile - 1) / kTile) > 1000 * ((items + sms - 1) / sms);
+}
+// The sums over the CTA's threads of (passes, blocks) of their long segments
+// (every thread calls it; tmp: two ints per warp).
+__device__ __forceinline__ void sum_pair(int& a, int& b, int* tmp, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    tmp[2 * (threadIdx.x >> 5)] = a;
+    tmp[2 * (threadIdx.x >> 5) + 1] = b;
+  }
+  __syncthreads();
+  a = b = 0;
+  for (int w = 0; w < warps; ++w) {
+    a += tmp[2 * w];
+    b += tmp[2 * w + 1];
+  }
+}
+
 // What the CTA shares.
 constexpr int kRedLane = 17;  // floats per lane (one more than 16: no bank conflicts)
 constexpr int kRed = kWarps * 32 * kRedLane;
 struct Shared {
   uint64_t bars[kWarps][kStages];
-  int wsum[kWarps];
+  int wsum[kWarps], pair[2 * kWarps];
   int abort;
   int* first;  // [N_r + 1] passes of xr rows before expert e
   int* off;    // [N_r + 1] the experts' segments
@@ -282,12 +317,26 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
   for (int e = tid; e <= P.N_r; e += kThreads) sh.off[e] = min(max(P.offsets[e], 0), n);
   __syncthreads();
   {  // exclusive scan of the experts' passes (thread i owns experts [i c, i c + c))
-    auto passes = [&](int e) {
-      const int rows = sh.off[e + 1] - sh.off[e];
-      return rows > 0 ? (rows + P.xr - 1) / P.xr : 0;
-    };
     const int c = (P.N_r + kThreads - 1) / kThreads;
     const int e0 = tid * c, e1 = e0 + c < P.N_r ? e0 + c : P.N_r;
+    bool without_long = false;
+    if (P.tile_rows > 0) {
+      int lp = 0, lb = 0;
+      for (int e = e0; e < e1; ++e) {
+        const int rows = sh.off[e + 1] - sh.off[e];
+        if (rows > P.tile_rows) {
+          lp += (rows + 15) / 16;
+          lb += (rows + kTileRows - 1) / kTileRows;
+        }
+      }
+      sum_pair(lp, lb, sh.pair, kWarps);
+      without_long = long_to_tile(lp, lb, P.n_out, P.sms);
+    }
+    auto passes = [&](int e) {
+      const int rows = sh.off[e + 1] - sh.off[e];
+      if (rows <= 0 || (without_long && rows > P.tile_rows)) return 0;
+      return (rows + P.xr - 1) / P.xr;
+    };
     int mine = 0;
     for (int e = e0; e < e1; ++e) mine += passes(e);
     int x = mine;
@@ -469,6 +518,9 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
     for (; used < requested; ++used)
       mbar_wait(smem_u32(&sh.bars[warp][used % kStages]), (uint32_t)(used / kStages) & 1u, abort,
                 true);
+  // a programmatic dependent of the many-row kernel, when that runs too: this
+  // one's end comes after both (they share nothing but their inputs)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace w4

@@ -16,6 +16,7 @@
 #include "ep.cuh"
 #include "expert_gemm.cuh"
 #include "expert_w4.cuh"
+#include "expert_w4_tile.cuh"
 #include "mr_common.cuh"
 #include "router_backward.cuh"
 #include "router_ffma.cuh"
@@ -1815,11 +1816,39 @@ int check_w4(int N_r, int n_out, int d, int group, int scale_dtype) {
 }
 
 template <int GROUP, typename S>
-int launch_expert_w4(const mr::w4::Params& P, unsigned grid, cudaStream_t s) {
+int launch_expert_w4(const mr::w4::Params& P, unsigned grid, int sms, cudaStream_t s) {
   auto kern = mr::w4::expert_w4_kernel<GROUP, S>;
   const int smem = mr::w4::smem_bytes(P.unit_bytes, P.N_r);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MR_ERR_CUDA;
+  const long n = (long)P.T * P.k;
+  if (P.tile_rows > 0) {  // some segment may be long: the many-row kernel, then this beside it
+    mr::w4t::Params Q;
+    Q.x = P.x;
+    Q.perm = P.perm;
+    Q.offsets = P.offsets;
+    Q.wp = P.wp;
+    Q.out = P.out;
+    Q.T = P.T;
+    Q.d = P.d;
+    Q.k = P.k;
+    Q.N_r = P.N_r;
+    Q.n_out = P.n_out;
+    Q.tiles = P.tiles;
+    Q.KB = P.KB;
+    Q.unit_bytes = P.unit_bytes;
+    Q.sms = P.sms;
+    auto tile = mr::w4t::expert_w4_tile_kernel<GROUP, S>;
+    constexpr int tile_smem = (int)mr::w4t::smem_bytes(sizeof(S) == 2 ? 2 : 3);
+    if (cudaFuncSetAttribute(tile, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem) !=
+        cudaSuccess)
+      return MR_ERR_CUDA;
+    const long blocks = n / mr::w4t::kRows + std::min<long>(n / (mr::w4t::kMinRows + 1), P.N_r);
+    const long items = blocks * ((P.n_out + mr::w4t::kOut - 1) / mr::w4t::kOut);
+    tile<<<(unsigned)std::min<long>(items, sms), mr::w4t::kThreads, (size_t)tile_smem, s>>>(Q);
+    if (launch_status() != MR_OK) return MR_ERR_CUDA;
+    return launch_pdl(kern, dim3(grid), dim3(mr::w4::kThreads), (size_t)smem, s, P);
+  }
   kern<<<grid, mr::w4::kThreads, (size_t)smem, s>>>(P);
   return launch_status();
 }
@@ -1881,6 +1910,10 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   // rows of x per pass over an expert's weights
   const long n = (long)T * k;
   P.xr = mr::w4::kRowsPerPass;
+  // the most passes that long segments can have (mr::w4::long_to_tile)
+  const long long_passes = n / 16 + n / (mr::w4::kLongRows + 1);
+  P.tile_rows = long_passes * l.tiles > 1000 ? mr::w4::kLongRows : 0;
+  P.sms = sms;
   const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
   // two CTAs per SM where their rings fit (all but fp32 scales of 32 columns, or
   // more than about 600 experts)
@@ -1888,13 +1921,13 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   const unsigned grid = (unsigned)std::min<long>(items, per_sm * sms);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (sb == 2) {
-    if (group == 32) return launch_expert_w4<32, uint16_t>(P, grid, s);
-    if (group == 64) return launch_expert_w4<64, uint16_t>(P, grid, s);
-    return launch_expert_w4<128, uint16_t>(P, grid, s);
+    if (group == 32) return launch_expert_w4<32, uint16_t>(P, grid, sms, s);
+    if (group == 64) return launch_expert_w4<64, uint16_t>(P, grid, sms, s);
+    return launch_expert_w4<128, uint16_t>(P, grid, sms, s);
   }
-  if (group == 32) return launch_expert_w4<32, float>(P, grid, s);
-  if (group == 64) return launch_expert_w4<64, float>(P, grid, s);
-  return launch_expert_w4<128, float>(P, grid, s);
+  if (group == 32) return launch_expert_w4<32, float>(P, grid, sms, s);
+  if (group == 64) return launch_expert_w4<64, float>(P, grid, sms, s);
+  return launch_expert_w4<128, float>(P, grid, sms, s);
 }
 
 // ---- expert parallelism over peer memory ------------------------------------
