@@ -155,11 +155,12 @@ def test_expert_w4_spread_magnitudes(spread):
     gr.check(widen(_host(out)), want, _bound(d, mag, magx), "bf16", "out")
 
 
+@pytest.mark.parametrize("T", [5, 600], ids=["few", "many"])
 @pytest.mark.parametrize("mode", ["eager", "graph"])
-def test_decode_step_of_a_moe_layer(mode):
+def test_decode_step_of_a_moe_layer(mode, T):
     """Gate, dispatch, experts on 4-bit weights, combine for a few tokens;
     against binary64 on the gate's own choice and weights."""
-    T, d, N_r, k, n_out, group = 5, 512, 32, 4, 512, 64
+    d, N_r, k, n_out, group = 512, 32, 4, 512, 64
     x, _, _, _, q, s = _problem(T, k, N_r, n_out, d, group, "bf16", 9)
     rng = np.random.default_rng(3)
     Wg = _f32(rng.standard_normal((N_r, d)) / np.sqrt(d))

@@ -6,8 +6,8 @@
 //
 // for the sorted row j of expert e, groups G of 32, 64 or 128 columns.  A few
 // rows per expert make this a stream of the hit experts' weights from HBM
-// (n_out * d / 2 bytes each plus the scales): the kernel's work per weight has
-// to stay below what the SMs issue while those bytes arrive: about 50 cycles
+// (n_out * d / 2 bytes each plus the scales): the kernel's work per weight
+// should stay below what the SMs issue while those bytes arrive, about 50 cycles
 // of an SM for 16 x 128 weights.  So
 //  * weights meet x in tensor-core MMAs with the weights as the 16-row operand
 //    and 8 rows of x as the columns (mma.sync m16n8k16: at this shape the
@@ -19,6 +19,13 @@
 //    shift; nothing is subtracted per weight: the sums start from -24 * sum x
 //    of the group's columns, which one more MMA pair with a constant operand
 //    forms for all rows at once.
+// Measured: 62 cycles per 16 x 128 weights (about 140 instructions, half of them
+// on the half-rate integer pipe), 66 % of the HBM rate on a decode batch of 64
+// tokens (434 us); the same kernel without the arithmetic streams at the full
+// rate (272 us).  Subtracting per weight instead took 557 us; 8-bit MMAs, whose
+// e4m3 codes 0 .. 15 are the nibbles themselves, run as two 16-bit ones with
+// unpacking on this GPU (639 us); a ring shared by the CTA with a producer warp
+// 643 us.
 // Every product is exact in fp32.  A group's sum runs through at most 55 * sum
 // |x| (24 + 31) where |q - 8| alone would reach 8 * sum |x|, in fp32; it is
 // then scaled and added in fp32, and the result rounded to bf16 once.
@@ -31,20 +38,21 @@
 // lane's share of x is 16 contiguous bytes -- its weights of step i are four
 // words (m = 0..3) for the first rows at 1024 i + 16 l and four for the second
 // at 1024 i + 512 + 16 l.  In a word, column 2 p of the eight is the nibble at
-// bit 3 + 4 p, column 2 p + 1 the one at bit 19 + 4 p (modulo 32).  The unit's scales follow
-// in their own type as [128 / group][8 rows l / 4][4 m][2], so that a lane
-// reads its eight scales of a step at once.  Padded rows and columns hold the
-// value 0 (nibble 8) and scale 0.
+// bit 3 + 4 p, column 2 p + 1 the one at bit 19 + 4 p (modulo 32).  The unit's
+// scales follow in their own type as [128 / group][8 rows l / 4][4 m][2], so
+// that a lane reads its eight scales of a step at once.  Padded rows and columns
+// hold the value 0 (nibble 8) and scale 0.
 //
 // The kernel is persistent, two CTAs per SM.  An item is 64 output rows of one
 // expert against up to `xr` of its sorted rows; a team of `ks` of the CTA's
-// eight warps (chosen from the number of items) takes it, splits its columns (member m takes units m, m + ks, ..)
-// and meets in shared memory at the item's end, adding in member order.  Each
-// warp has its own ring of units
-// in shared memory, filled by one bulk copy each, and requests a unit as soon
-// as it has finished the one whose place it takes, through the ends of items,
-// so that the stream from HBM does not pause; no warp waits for another but its
-// team at an item's end.  x comes through L1.  Every mbarrier wait is bounded.
+// eight warps (chosen from the number of items) takes it, splits its columns
+// (member m takes units m, m + ks, ..) and meets in shared memory at the item's
+// end, adding in member order.  Each warp has its own ring of units in shared
+// memory, filled by one bulk copy each, and requests a unit as soon as it has
+// finished the one whose place it takes, through the ends of items, so that the
+// stream from HBM does not pause; no warp waits for another but its team at an
+// item's end.  x comes through L1.  Every mbarrier wait is bounded.
+// Segments of many rows may go to expert_w4_tile.cuh's kernel (long_to_tile).
 #pragma once
 
 #include <type_traits>
@@ -501,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
         const int row = t * 8 + c, col = k.tile * kTile + r;
         if (row < k.rows && col < P.n_out && !*abort) {
           const __nv_bfloat16 b = __float2bfloat16_rn(v);
-          P.out[(long)(k.row0 + row) * P.n_out + col] = *reinterpret_cast<const uint16_t*>(&b);
+          P.out[(long)(k.row0 + row) * P.n_out + col] =
+              *reinterpret_cast<const uint16_t*>(&b);
         }
       }
     }

@@ -14,8 +14,7 @@
 //
 // tcgen05 kind::f16, M = 128 (output rows), N = 16 .. 192 (rows of x, rounded up
 // to 16), K staged 64 at a time (128-byte swizzled rows).  The rows of x and the
-// widened weights have rings of their own, so that the copies run five stages
-// ahead (with one ring of three, a stage took the latency of a copy, 0.77 us).
+// widened weights have rings of their own.
 //   warp 0       TMEM owner and MMA issuer (one elected thread)
 //   warps 1-4    rows of x, 16 bytes a copy (cp.async); at the end TMEM -> bf16
 //                -> out
@@ -27,11 +26,12 @@
 // kernel is faster); one CTA per SM takes items blockIdx.x, + gridDim.x,
 // .. (only the device knows how many there are).  Every mbarrier wait is bounded.
 //
-// The widening bounds it up to about 100 rows (bf16 scales) or at any number
-// (fp32 scales, about 16 instructions for two weights): hence the sixteen warps
-// for it, and one block for a segment where blocks of 128 rows would widen its
-// weights twice (150 rows x 8 experts, d = 1408, n_out = 2056, fp32 scales: 67 us
-// with 128 rows and eight warps, 36 us so).
+// The widening bounds it (a stage takes 0.7 us, whatever the rows): hence the
+// sixteen warps for it, and one block for a segment where blocks of 128 rows
+// would widen its weights twice.  Measured: 150 rows x 8 experts (d = 1408, n_out
+// = 2056, fp32 scales) 67 us with blocks of 128 rows, eight warps and a CTA for
+// every block there might be, 39 us so; 128 rows x 256 experts (d = 7168, n_out =
+// 2048) 3.3 ms, 295 TFLOP/s.
 #pragma once
 
 #include <type_traits>
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
           for (int kk = 0; kk < kK / 16; ++kk)
 #pragma unroll
             for (int p = NP - 1; p >= 0; --p)  // the small plane first
-              mma_bf16(tmem_base, make_desc(a + p * kPlane + kk * 32), make_desc(b + kk * 32), idesc,
-                       (kc > 0 || kk > 0 || p < NP - 1) ? 1u : 0u);
+              mma_bf16(tmem_base, make_desc(a + p * kPlane + kk * 32), make_desc(b + kk * 32),
+                       idesc, (kc > 0 || kk > 0 || p < NP - 1) ? 1u : 0u);
           mma_commit(bar(B_XEMPTY + xp.s));
           mma_commit(bar(B_WEMPTY + wp.s));
         }
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
         for (int i = 0; i < 16; ++i) {
           if (c0 + i >= rows) break;
           const __nv_bfloat16 b = __float2bfloat16_rn(v[i]);
-          P.out[(long)(row0 + c0 + i) * P.n_out + col] = *reinterpret_cast<const uint16_t*>(&b);
+          P.out[(long)(row0 + c0 + i) * P.n_out + col] =
+              *reinterpret_cast<const uint16_t*>(&b);
         }
       }
     } else {
@@ -335,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       const int u2 = wd >> 2, h = (wd >> 1) & 1, mh = wd & 1;
       const int tile = out0 / w4::kTile + u2;
       const bool here = tile < P.tiles;
-      const uint8_t* src = P.wp + ((long)e * P.tiles + (here ? tile : 0)) * P.KB * (long)P.unit_bytes;
+      const uint8_t* src =
+          P.wp + ((long)e * P.tiles + (here ? tile : 0)) * P.KB * (long)P.unit_bytes;
       // the words and the scales (m, then h; as loaded) of the next two stages
       using Sc = typename std::conditional<sizeof(S) == 2, uint2, uint4>::type;
       uint2 w[2][2];
@@ -346,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int i = (kc & 1) * 2 + j;
-          w[b][j] = __ldg(reinterpret_cast<const uint2*>(unit + 1024 * i + 512 * h + 16 * lane) + mh);
+          w[b][j] =
+              __ldg(reinterpret_cast<const uint2*>(unit + 1024 * i + 512 * h + 16 * lane) + mh);
           sc[b][j] = __ldg(reinterpret_cast<const Sc*>(unit + w4::kWeightBytes) +
                            ((i * 32 / GROUP) * 8 + lane / 4) * 2 + mh);
         }

@@ -21,7 +21,9 @@
 // Persistent: CTA i takes the tiles i, i + gridDim.x, ..; the producer and the
 // MMA run on into the next tile while the workers write one.  dW may split K
 // (P.splits slices, summed in order afterwards).  Every mbarrier wait is
-// bounded.
+// bounded.  Measured at T = 4096, d = 7168, N_r = 256: dx 86 us (six products, 1.05
+// PFLOP/s issued), dW 53 us (three, 0.85 PFLOP/s: 53 bytes a cycle and SM of
+// operands through L2); fp32 on the CUDA cores took 547 and 643 us.
 #pragma once
 
 #include "router_tc.cuh"
