@@ -239,10 +239,10 @@ __device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const ui
 // Whether the segments of more than kLongRows rows go to the many-row kernel
 // (expert_w4_tile.cuh), decided alike by both kernels from the segments:
 // `passes` passes of 16 of their rows here, or `blocks` blocks there.  There a
-// 128-row tile of n_out takes an SM 0.7 us for 64 columns, however few the
+// 128-row tile of n_out takes an SM 0.6 us for 64 columns, however few the
 // blocks; here a unit and pass takes the whole GPU about 1.4 ns.  Measured (d =
 // 7168, n_out = 2048), here / there: 1 x 128 rows 32 / 96 us, 8 x 48 rows 88 / 84,
-// 8 x 128 rows 150 / 99, 256 x 128 rows 3.7 / 2.9 ms.
+// 8 x 128 rows 150 / 90, 256 x 128 rows 3.7 / 2.3 ms.
 constexpr int kLongRows = 32;
 constexpr int kTileRows = 192;  // rows per block there
 __device__ __forceinline__ bool long_to_tile(long passes, long blocks, int n_out, int sms) {

@@ -20,18 +20,20 @@
 //                -> out
 //   warps 5-20   weights: two sets of eight warps take the stages in turn; each
 //                lane widens 4 x 8 weights, the words and scales of its set's
-//                next two stages already on their way
+//                next three stages already on their way
 // An item is a block of up to 192 rows of a segment of more than kMinRows rows
 // and a 128-row tile of n_out (none when long_to_tile says that the few-row
 // kernel is faster); one CTA per SM takes items blockIdx.x, + gridDim.x,
 // .. (only the device knows how many there are).  Every mbarrier wait is bounded.
 //
-// The widening bounds it (a stage takes 0.7 us, whatever the rows): hence the
-// sixteen warps for it, and one block for a segment where blocks of 128 rows
-// would widen its weights twice.  Measured: 150 rows x 8 experts (d = 1408, n_out
-// = 2056, fp32 scales) 67 us with blocks of 128 rows, eight warps and a CTA for
-// every block there might be, 39 us so; 128 rows x 256 experts (d = 7168, n_out =
-// 2048) 3.3 ms, 295 TFLOP/s.
+// Shared memory bounds it: at 128 rows a stage writes 32 KB of widened weights
+// (two planes) and 16 KB of x, and its MMAs read 64 KB, about 900 of the 1150
+// cycles it takes; the widening itself is hidden (sixteen warps).  One block for
+// a segment where blocks of 128 rows would widen its weights twice.  Measured:
+// 150 rows x 8 experts (d = 1408, n_out = 2056, fp32 scales) 67 us with blocks of
+// 128 rows, eight warps and a CTA for every block there might be, 39 us so; 128
+// rows x 256 experts (d = 7168, n_out = 2048) 2.6 ms with the rows' addresses
+// formed for every copy, 2.3 ms so; eight or twelve copy warps 2.4 and 2.6 ms.
 #pragma once
 
 #include <type_traits>
@@ -282,6 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       const uint32_t dst0 = (uint32_t)r0 * 128u + ((uint32_t)(c ^ (r0 & 7)) << 4);
       constexpr int kCopies = kRows / 16;  // 16 rows of 8 chunks per round
       static_assert(32 * kCopyWarps == 16 * 8, "a round copies 16 rows");
+      const uint16_t* from[kCopies];
+#pragma unroll
+      for (int u = 0; u < kCopies; ++u) from[u] = P.x + (long)tok_s[r0 + 16 * u] * P.d + c * 8;
       Place<kXStages> xp(g0), lag(g0);
       for (int kc = 0; kc < KC; ++kc, xp.step()) {
         if (kc >= kLag) {
@@ -294,13 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
         }
         const uint32_t base = x0 + xp.s * kXBytes + dst0;
         const int col = kc * kK + c * 8;
-        const uint16_t* xc = P.x + (col < P.d ? col : 0);
-        const uint32_t bytes = col < P.d ? 16u : 0u;  // columns past d: zeros
+        // columns past d: zeros (nothing is read)
+        const uint32_t bytes = col < P.d ? 16u : 0u;
+        const int at = col < P.d ? kc * kK : 0;
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
           if (16 * u >= n_rows) break;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + u * 2048),
-                       "l"(xc + (long)tok_s[r0 + 16 * u] * P.d), "r"(bytes)
+                       "l"(from[u] + at), "r"(bytes)
                        : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -338,10 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       const bool here = tile < P.tiles;
       const uint8_t* src =
           P.wp + ((long)e * P.tiles + (here ? tile : 0)) * P.KB * (long)P.unit_bytes;
-      // the words and the scales (m, then h; as loaded) of the next two stages
+      // the words and the scales (m, then h; as loaded) of the next kAhead stages;
+      // each buffer is loaded again as soon as it has been read (moving them up
+      // would wait for the newest)
       using Sc = typename std::conditional<sizeof(S) == 2, uint2, uint4>::type;
-      uint2 w[2][2];
-      Sc sc[2][2];
+      constexpr int kAhead = 3;
+      uint2 w[kAhead][2];
+      Sc sc[kAhead][2];
       auto fetch = [&](int kc, int b) {
         if (!here || kc >= KC) return;
         const uint8_t* unit = src + (long)(kc >> 1) * P.unit_bytes;
@@ -358,26 +367,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       // quarter warp's 16-byte stores (two rows) fall on distinct banks.
       const bool odd = (lane / 4) & 1;
       const uint32_t row = (uint32_t)(u2 * 64 + mh * 32 + 8 * h + lane / 4);
-      fetch(set, 0);
-      fetch(set + kWidenSets, 1);
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) fetch(set + b * kWidenSets, b);
       Place<kWStages> wp(g0 + set);
-      for (int kc = set; kc < KC; kc += kWidenSets, wp.step(kWidenSets)) {
+      auto widen = [&](int kc, int b) {  // false: a wait gave up
         uint2 wc[2];
         Sc scc[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          wc[j] = odd ? w[0][1 - j] : w[0][j];
-          scc[j] = odd ? sc[0][1 - j] : sc[0][j];
+          wc[j] = odd ? w[b][1 - j] : w[b][j];
+          scc[j] = odd ? sc[b][1 - j] : sc[b][j];
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          w[0][j] = w[1][j];
-          sc[0][j] = sc[1][j];
-        }
-        fetch(kc + 2 * kWidenSets, 1);
+        fetch(kc + kAhead * kWidenSets, b);
         if (g0 + kc >= kWStages &&
             !__all_sync(0xffffffffu, mbar_wait(bar(B_WEMPTY + wp.s), wp.ph ^ 1u, abort)))
-          break;
+          return false;
         if (here) {
           uint8_t* a = smem + kXStages * kXBytes + wp.s * NP * kPlane + row * 128;
 #pragma unroll
@@ -405,6 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_WFULL + wp.s));
+        wp.step(kWidenSets);
+        return true;
+      };
+      bool go = true;
+      for (int kc = set; kc < KC && go; kc += kAhead * kWidenSets) {
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b)
+          if (go && kc + b * kWidenSets < KC) go = widen(kc + b * kWidenSets, b);
       }
     }
     tc_fence_before();
