@@ -47,6 +47,17 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// c + a * b of two independent fp32 pairs in one instruction (each rounded as a
+// scalar fused multiply-add).
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a, float b0, float b1) {
+  uint64_t c, aa, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(aa), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(c));
+}
+
 // One warp per token.  Sigmoid: slot[t*k + j] = dl_j (0 for an id outside
 // [0, N_r)); `dense` (optional) gets the whole row dL[t].  Softmax: slot is not
 // written; `dense` gets the row and `planes` its three bf16 planes [3][T][Np]
@@ -125,24 +136,22 @@ __global__ void __launch_bounds__(32 * kDlWarps)
 // from shared memory (128 bytes a cycle and SM), which is what bounds the
 // kernel, instead of L2.  The grid is one wave: the (column chunk, block of
 // tokens) pairs are dealt out evenly, so a CTA loads its columns of W once or
-// twice.  A warp takes kDxTokens tokens at a time (independent
-// reads in flight) and stages their (row, dl) pairs in its own piece of shared
-// memory, the next tokens' already on their way (addv may be dxv: neither is
-// __restrict__).
+// twice.  A warp takes kDxTokens tokens at a time (independent reads in flight)
+// and stages their (row, dl) pairs in its own piece of shared memory, the next
+// tokens' already on their way (addv may be dxv: neither is __restrict__).
 //
 // The kernel is a programmatic dependent of dlogits_kernel: W is loaded while
 // that runs.  Measured on the full DeepSeek-V3 batch (16384 tokens, 256
-// experts, with add): 170-180 us with dlogits_kernel, against 118 us for the reads
-// of shared memory alone; 1024 threads of 64 registers 205 us (spills), one
-// token per warp at a time 435 us.  It lets dw_slots_kernel start as its CTAs
-// finish (345 us for the whole call against 356 us one after the other); making
-// room for both on an SM (80 registers a thread) gained nothing, the spills
-// cost what the overlap saved.
+// experts, with add): 167 us with dlogits_kernel, against 118 us for the reads of
+// shared memory alone; without the paired multiply-adds 180 us; 1024 threads of
+// 64 registers 205 us (spills), one token per warp at a time 435 us.  It lets
+// dw_slots_kernel start as its CTAs finish (10 us less for the whole call than
+// one after the other); making room for both on an SM (80 registers a thread)
+// gained nothing, the spills cost what the overlap saved.
 constexpr int kDxThreads = 512;
 constexpr int kDxTokens = 4;
 // (row, dl) pairs per lane of a warp's tokens: one for k <= 8, else up to four
 constexpr int kDxSmall = (kDxTokens * 8 + 31) / 32, kDxLarge = kDxTokens * kMaxK / 32;
-constexpr int dx_pairs_per_lane(int k) { return k <= 8 ? kDxSmall : kDxLarge; }
 
 __host__ __device__ constexpr size_t dx_smem_bytes(int N_r, int cw, int k) {
   // two buffers per warp of kDxTokens rows of pairs, each padded to an even count
@@ -273,10 +282,10 @@ __global__ void __launch_bounds__(kDxThreads)
           if constexpr (VEC && CPL == 4) {
             const float4 v0 = *reinterpret_cast<const float4*>(w0 + lane * 4);
             const float4 v1 = *reinterpret_cast<const float4*>(w1 + lane * 4);
-            acc[u][0] = fmaf(a1, v1.x, fmaf(a0, v0.x, acc[u][0]));
-            acc[u][1] = fmaf(a1, v1.y, fmaf(a0, v0.y, acc[u][1]));
-            acc[u][2] = fmaf(a1, v1.z, fmaf(a0, v0.z, acc[u][2]));
-            acc[u][3] = fmaf(a1, v1.w, fmaf(a0, v0.w, acc[u][3]));
+            fma2(acc[u][0], acc[u][1], a0, v0.x, v0.y);
+            fma2(acc[u][2], acc[u][3], a0, v0.z, v0.w);
+            fma2(acc[u][0], acc[u][1], a1, v1.x, v1.y);
+            fma2(acc[u][2], acc[u][3], a1, v1.z, v1.w);
           } else {
 #pragma unroll
             for (int i = 0; i < CPL; ++i)
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(kDxThreads)
 // stay in L2 while every expert reads them).  An expert's first piece goes to
 // dW, the others to `part`, and dw_join_kernel adds them in order: no atomics, a
 // long segment is spread over many SMs.  Bound by L2: T * k rows of x pass from
-// there to the SMs, 12 TB/s on the full DeepSeek-V3 batch (157 us; pieces of 512
+// there to the SMs, 12 TB/s on the full DeepSeek-V3 batch (151 us; pieces of 512
 // rows make the whole call 14 us longer).
 constexpr int kDwRows = 256;
 constexpr int kDwThreads = 128;
@@ -470,8 +479,12 @@ __global__ void __launch_bounds__(kDwThreads)
         const float g = r + u < pc.rows ? gs[r + u] : 0.0f;
         float xf[NE];
         R::unpack(xv[u], xf);
+        if constexpr (NE % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] = fmaf(g, xf[i], acc[i]);
+          for (int i = 0; i < NE; i += 2) fma2(acc[i], acc[i + 1], g, xf[i], xf[i + 1]);
+        } else {
+          acc[0] = fmaf(g, xf[0], acc[0]);
+        }
       }
     }
     const long d = nvec * NE;
