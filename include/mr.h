@@ -682,7 +682,9 @@ int mr_gather_rows_backward(const void *dxs, int dtype,
  * of perm out of range inside a segment, or offsets that overlap, raise the
  * device flag (MR_ERR_DEVICE).  Calls that may overlap need different
  * workspaces.
- * Limits: N_r <= 512, 1 <= k <= 32; at least one of dlogits, dx and dW.
+ * Limits: N_r <= 512, 1 <= k <= 32, at least one of dlogits, dx and dW; sizes
+ * past a launch's grid (rows of 8 million elements that no vector fits, softmax
+ * with 8 million tokens off the tensor cores) return MR_ERR_UNSUPPORTED.
  */
 size_t mr_router_backward_workspace_size(int T, int d, int N_r, int k,
                                          int flags);

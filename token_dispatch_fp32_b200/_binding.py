@@ -621,7 +621,7 @@ def mr_expert_gemv_gather_w4(x, k, perm, offsets, packed, N_r, n_out, group,
     _need(x, "x", torch.bfloat16)
     T, d = x.shape
     if perm is None:
-        if T % k:
+        if k <= 0 or T % k:
             raise ValueError("without perm, x must have T*k rows")
         T //= k
     else:

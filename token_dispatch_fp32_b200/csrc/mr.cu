@@ -1400,6 +1400,30 @@ int mr_combine(const void* expert_out, int dtype, const float* w, const int32_t*
 
 namespace {
 
+// Launch as a programmatic dependent of the previous kernel on the stream (the
+// kernel itself waits for that one's results with griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+               Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MR_ERR_CUDA;
+  }
+  return MR_OK;
+}
+
 template <typename V, bool BF16>
 int launch_combine_backward(const void* dy, const void* E, const float* w, const int32_t* inv,
                             void* dE, float* dw, int T, long nvec, int k, cudaStream_t s) {
@@ -1484,8 +1508,8 @@ int launch_planes(const CUtensorMap& ma, const CUtensorMap& mb, const mr::pg::Ge
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MR_ERR_CUDA;
   const int items = P.m_tiles * P.n_tiles * P.splits;
-  kern<<<(unsigned)std::min(items, sms), mr::tc::kThreads, (size_t)smem, s>>>(ma, mb, P);
-  return launch_status();
+  return launch_pdl(kern, dim3((unsigned)std::min(items, sms)), dim3(mr::tc::kThreads),
+                    (size_t)smem, s, ma, mb, P);
 }
 
 mr::pg::GemmParams gemm_params(int M, int N, int K, int splits, const void* add, void* out) {
@@ -1536,30 +1560,6 @@ int launch_dw_planes(const void* planes, const void* x, float* out, int T, int d
       !make_map_planes(&mb, x, d, T, 1, d, 64, mr::pg::kBK, CU_TENSOR_MAP_SWIZZLE_128B))
     return MR_ERR_CUDA;
   return launch_planes<true, 1, false>(ma, mb, gemm_params(N_r, d, T, slices, nullptr, out), sms, s);
-}
-
-// Launch as a programmatic dependent of the previous kernel on the stream (the
-// kernel itself waits for that one's results with griddepcontrol.wait).
-template <typename... KArgs, typename... Args>
-int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-               Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return MR_ERR_CUDA;
-  }
-  return MR_OK;
 }
 
 struct DxArgs {
@@ -1615,6 +1615,7 @@ int launch_dw_slots(const void* x, const int32_t* perm, const int32_t* offsets, 
                     cudaStream_t s) {
   const unsigned pieces = (unsigned)((n + mr::rb::kDwRows - 1) / mr::rb::kDwRows + N_r);
   const unsigned slabs = (unsigned)((nvec + mr::rb::kDwThreads - 1) / mr::rb::kDwThreads);
+  if (slabs > 65535) return MR_ERR_UNSUPPORTED;
   return launch_pdl(mr::rb::dw_slots_kernel<V, BF16>, dim3(pieces, slabs),
                     dim3(mr::rb::kDwThreads), 0, s, static_cast<const V*>(x), perm, offsets, slot,
                     n, N_r, k, nvec, dW, part, !after_dx);
@@ -1626,6 +1627,7 @@ int launch_dense(const float* A, const void* B, bool b_bf16, const void* add, vo
                  bool out_bf16, int M, int N, int K, int slices, cudaStream_t s) {
   const dim3 grid((unsigned)((N + mr::rb::kGemmT - 1) / mr::rb::kGemmT),
                   (unsigned)((M + mr::rb::kGemmT - 1) / mr::rb::kGemmT), (unsigned)slices);
+  if (grid.y > 65535) return MR_ERR_UNSUPPORTED;
   if (out_bf16) {
     if (b_bf16) mr::rb::dense_kernel<TA, true, true><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);
     else mr::rb::dense_kernel<TA, false, true><<<grid, 256, 0, s>>>(A, B, add, C, M, N, K);

@@ -120,6 +120,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
+  // a programmatic dependent of the kernel before it: the set-up above runs
+  // while that one ends
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int KC = (P.K + kBK - 1) / kBK;
   const int items = P.m_tiles * P.n_tiles * P.splits;
