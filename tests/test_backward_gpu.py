@@ -417,6 +417,34 @@ def test_two_gradients_at_once():
         del got
 
 
+@pytest.mark.parametrize("flags", [0, mr.MR_SCORE_SOFTMAX])
+def test_workspace_of_a_call_on_a_named_stream(flags):
+    """stream= without a workspace: the one the call allocates is not handed to
+    work of the current stream while the call still waits to run."""
+    T, d, N_r, k = 700, 1024, 64, 4
+    _, x, W, L, idx, g = _gate_problem(T, d, N_r, k, "bf16", "f32", 0, seed=3)
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    args = (_dev(x), _dev(W), _f32(L), _i32(idx), _f32(g), _i32(perm), _i32(offsets), 2.5, flags)
+    ref = mr.mr_router_backward(*args)
+    dref = mr.mr_dispatch(args[3], N_r)
+    s = torch.cuda.Stream()
+    size = max(mr.mr_router_backward_workspace_size(T, d, N_r, k, flags), 16)
+    dsize = max(mr.mr_dispatch_workspace_size(T, k, N_r), 4)
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # some ten milliseconds
+        got = mr.mr_router_backward(*args, stream=s)
+        dgot = mr.mr_dispatch(args[3], N_r, stream=s)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                for n in (size, size, dsize, dsize)]
+        torch.cuda.synchronize()
+        del junk
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        assert all(torch.equal(a, b) for a, b in zip(dgot, dref))
+        del got, dgot
+
+
 def test_wrong_arguments_are_refused():
     T, d, k, N_r = 4, 16, 2, 8
     dy = torch.zeros((T, d), device="cuda")

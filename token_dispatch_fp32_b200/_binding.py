@@ -150,6 +150,16 @@ def _call(fn: str, dev, stream, *args) -> None:
         raise MRError(fn, status)
 
 
+def _scratch(nbytes, dev, stream):
+    """A workspace for one call on `stream` (None: the current stream).  It is
+    freed when the call returns, so it comes from that stream's own memory: the
+    allocator hands it out again behind the call's kernels, never beside them."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def _device_of(*tensors):
     """The one CUDA device of the given tensors (None entries ignored)."""
     dev = None
@@ -306,7 +316,7 @@ def mr_dispatch(idx, N_r, counts=None, offsets=None, perm=None, inv_perm=None, w
         _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     need = mr_dispatch_workspace_size(T, k, N_r)
     if workspace is None:
-        workspace = torch.empty(max(need, 4), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(need, 4), dev, stream)
     _need(workspace, "workspace")
     _call("mr_dispatch", _device_of(idx, counts, offsets, perm, inv_perm, workspace), stream,
           _ptr(idx), T, k, N_r, _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv_perm),
@@ -582,8 +592,8 @@ def mr_router_backward(x, W, logits, idx, dw, perm, offsets, route_scale, flags=
     elif want_dW:
         dW = torch.empty((N_r, d), dtype=torch.float32, device=x.device)
     if workspace is None:
-        workspace = torch.empty(max(mr_router_backward_workspace_size(T, d, N_r, k, flags), 16),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _scratch(max(mr_router_backward_workspace_size(T, d, N_r, k, flags), 16),
+                             x.device, stream)
     _need(workspace, "workspace")
     _call("mr_router_backward", _device_of(x, W, logits, idx, dw, perm, offsets, add, dlogits, dx,
                                            dW, workspace), stream,

@@ -21,7 +21,7 @@
 //    forms for all rows at once.
 // Measured: 62 cycles per 16 x 128 weights (about 140 instructions, half of them
 // on the half-rate integer pipe), 66 % of the HBM rate on a decode batch of 64
-// tokens (434 us); the same kernel without the arithmetic streams at the full
+// tokens (422 to 442 us); the same kernel without the arithmetic streams at the full
 // rate (272 us).  Subtracting per weight instead took 557 us; 8-bit MMAs, whose
 // e4m3 codes 0 .. 15 are the nibbles themselves, run as two 16-bit ones with
 // unpacking on this GPU (639 us); a ring shared by the CTA with a producer warp

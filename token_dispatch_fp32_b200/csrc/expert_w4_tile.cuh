@@ -31,7 +31,7 @@
 // cycles it takes; the widening itself is hidden (sixteen warps).  One block for
 // a segment where blocks of 128 rows would widen its weights twice.  Measured:
 // 150 rows x 8 experts (d = 1408, n_out = 2056, fp32 scales) 67 us with blocks of
-// 128 rows, eight warps and a CTA for every block there might be, 39 us so; 128
+// 128 rows, eight warps and a CTA for every block there might be, 37 us so; 128
 // rows x 256 experts (d = 7168, n_out = 2048) 2.6 ms with the rows' addresses
 // formed for every copy, 2.3 ms so; eight or twelve copy warps 2.4 and 2.6 ms.
 #pragma once
