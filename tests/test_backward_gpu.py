@@ -149,6 +149,20 @@ def test_row_gradients_on_unaligned_buffers(dtype, off):
     assert torch.equal(dx, mr.mr_gather_rows_backward(_dev(E), k, _i32(inv), add=_dev(dy)))
 
 
+@pytest.mark.parametrize("T,d,k,N_r,dtype", [
+    (700, 2048, 6, 64, "bf16"),   # the widest rows of small CTAs, 32-byte vectors
+    (700, 2064, 6, 64, "bf16"),   # one vector more
+    (300, 1032, 4, 16, "f32"),    # 32-byte vectors, one more than small CTAs take
+    (300, 1020, 32, 40, "f32"),   # 16-byte vectors, k = 32
+    (300, 511, 5, 16, "bf16"),    # elements, small CTAs
+    (300, 513, 32, 40, "bf16"),   # elements, one more
+    (9000, 24, 2, 16, "bf16"),    # more tokens than CTAs at once, few vectors
+])
+def test_row_gradients_of_narrow_rows(T, d, k, N_r, dtype):
+    test_combine_backward(T, d, k, N_r, dtype)
+    test_gather_backward(T, d, k, N_r, dtype, True)
+
+
 # ---- gate -----------------------------------------------------------------------------------
 
 GATE = [  # T, d, N_r, k, x, W, hot experts
@@ -212,6 +226,45 @@ def test_router_backward(T, d, N_r, k, xdt, wdt, hot, softmax):
     if add is not None:  # in place
         mr.mr_router_backward(*args, *plan, 2.5, flags=flags, add=dadd, dx=dadd, want_dW=False)
         assert torch.equal(dadd, dx)
+
+
+@pytest.mark.parametrize("T,k,hot", [(2048, 8, 0), (4096, 8, 8), (9000, 8, 9)],
+                         ids=["64", "128", "256"])
+def test_router_backward_piece_sizes(T, k, hot):
+    """Segments in pieces of 64, 128 and 256 rows (the other cases have 32)."""
+    test_router_backward(T, 2048, 24, k, "bf16", "f32", hot, False)
+
+
+@pytest.mark.parametrize("d", [1, 2, 3, 1020, 1021, 1022, 1023, 2043, 2045])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("T", [1, 2, 70])
+def test_gate_weight_gradient_of_rows_inside_words(T, d, off):
+    """bf16 rows of any width and start: what lies before and behind x (NaN)
+    and a neighbouring row's ends (infinite) stay out of a row's sums."""
+    N_r, k = 6, 2
+    rng, x, W, L, idx, g = _gate_problem(T, d, N_r, k, "bf16", "f32", 0, seed=T + d)
+    if T > 2:
+        idx[:, 0], idx[:, 1] = rng.integers(0, 3, T), rng.integers(3, 5, T)  # 5: no rows
+        idx[T // 2] = 0, 5  # the only row of expert 5
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    buf = torch.full((T * d + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    view = buf[8 + off:8 + off + T * d].view(T, d)
+    view.copy_(_dev(x))
+    args = (_dev(W), _f32(L), _i32(idx), _f32(g), _i32(perm), _i32(offsets), 2.5)
+    dlog = torch.empty((T, N_r), device="cuda")
+    _, dW = mr.mr_router_backward(view, *args, dlogits=dlog, want_dx=False)
+    assert mr.mr_get_error() == mr.MR_OK
+    dL, err = gr.dlogits(L, idx, g, 2.5, False, 1e-20)
+    _, _, rW, bW = gr.products(dL, err, widen(x), widen(W), None)
+    gr.check(dW.cpu().numpy(), rW, bW, "f32", "dW")
+    if T <= 2:
+        return
+    t = T // 2
+    view[t - 1, d - 1] = float("inf")
+    view[t + 1, 0] = float("inf")
+    _, dW2 = mr.mr_router_backward(view, *args, want_dx=False)
+    assert torch.equal(dW2[5], dW[5])  # expert 5 has row t alone
+    assert torch.equal(dW2[:, 1:d - 1], dW[:, 1:d - 1])
 
 
 @pytest.mark.parametrize("softmax", [False, True], ids=["sigmoid", "softmax"])

@@ -1427,19 +1427,28 @@ int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaS
 template <typename V, bool BF16>
 int launch_combine_backward(const void* dy, const void* E, const float* w, const int32_t* inv,
                             void* dE, float* dw, int T, long nvec, int k, cudaStream_t s) {
-  mr::combine_backward_kernel<V, BF16><<<(unsigned)T, mr::kRowThreads, 0, s>>>(
-      static_cast<const V*>(dy), static_cast<const V*>(E), w, inv, static_cast<V*>(dE), dw, nvec,
-      k);
-  return launch_status();
+  auto launch = [&](auto kern, int threads) {
+    kern<<<(unsigned)T, threads, 0, s>>>(static_cast<const V*>(dy), static_cast<const V*>(E), w,
+                                         inv, static_cast<V*>(dE), dw, nvec, k);
+    return launch_status();
+  };
+  return mr::small_rows<V>(nvec)
+             ? launch(mr::combine_backward_kernel<V, BF16, mr::kRowSmall>, mr::kRowSmall)
+             : launch(mr::combine_backward_kernel<V, BF16, mr::kRowThreads>, mr::kRowThreads);
 }
 
 template <typename V, bool BF16>
 int launch_gather_backward(const void* dxs, const int32_t* inv, const void* add, void* dx, int T,
-                           long nvec, int k, unsigned grid, cudaStream_t s) {
-  mr::gather_backward_kernel<V, BF16><<<grid, mr::kRowThreads, 0, s>>>(
-      static_cast<const V*>(dxs), inv, static_cast<const V*>(add), static_cast<V*>(dx), T, nvec,
-      k);
-  return launch_status();
+                           long nvec, int k, int sms, cudaStream_t s) {
+  auto launch = [&](auto kern, int threads, int per_sm) {
+    kern<<<(unsigned)std::min<long>(T, (long)sms * per_sm), threads, 0, s>>>(
+        static_cast<const V*>(dxs), inv, static_cast<const V*>(add), static_cast<V*>(dx), T, nvec,
+        k);
+    return launch_status();
+  };
+  return mr::small_rows<V>(nvec)
+             ? launch(mr::gather_backward_kernel<V, BF16, mr::kRowSmall>, mr::kRowSmall, 32)
+             : launch(mr::gather_backward_kernel<V, BF16, mr::kRowThreads>, mr::kRowThreads, 16);
 }
 
 // Workspace of mr_router_backward: the slots' logit gradients (sigmoid), or
@@ -1480,7 +1489,8 @@ RouterBwdWs router_bwd_ws(int T, int d, int N_r, int k, int flags) {
     w.part = take(w.slices > 1 ? (size_t)w.slices * N_r * d * sizeof(float) : 0);
   } else {
     w.slot = take((size_t)T * k * sizeof(float));
-    w.part = take((size_t)((long)T * k / mr::rb::kDwRows) * d * sizeof(float));
+    const long n = (long)T * k;
+    w.part = take((size_t)(n >> mr::rb::dw_piece_shift(n, d)) * d * sizeof(float));
   }
   w.total = at;
   return w;
@@ -1611,14 +1621,14 @@ int launch_dx(const DxArgs& a) {
 
 template <typename V, bool BF16>
 int launch_dw_slots(const void* x, const int32_t* perm, const int32_t* offsets, const float* slot,
-                    int n, int N_r, int k, long nvec, float* dW, float* part, bool after_dx,
-                    cudaStream_t s) {
-  const unsigned pieces = (unsigned)((n + mr::rb::kDwRows - 1) / mr::rb::kDwRows + N_r);
-  const unsigned slabs = (unsigned)((nvec + mr::rb::kDwThreads - 1) / mr::rb::kDwThreads);
+                    int n, int N_r, int k, int sh, long nvec, float* dW, float* part,
+                    bool after_dx, cudaStream_t s) {
+  const unsigned pieces = (unsigned)((((long)n + (1 << sh) - 1) >> sh) + N_r);
+  const unsigned slabs = mr::rb::DwShape<V, BF16>::slabs(nvec);
   if (slabs > 65535) return MR_ERR_UNSUPPORTED;
   return launch_pdl(mr::rb::dw_slots_kernel<V, BF16>, dim3(pieces, slabs),
                     dim3(mr::rb::kDwThreads), 0, s, static_cast<const V*>(x), perm, offsets, slot,
-                    n, N_r, k, nvec, dW, part, !after_dx);
+                    n, N_r, k, sh, nvec, dW, part, !after_dx);
 }
 
 // C = A . B on the CUDA cores (mr::rb::dense_kernel).
@@ -1685,19 +1695,18 @@ int mr_gather_rows_backward(const void* dxs, int dtype, const int32_t* inv_perm,
   const bool bf16 = dtype == MR_BF16;
   const long row_bytes = (long)d * (bf16 ? 2 : 4);
   auto all = [&](bool (*ok)(const void*)) { return ok(dxs) && ok(dx) && (!add || ok(add)); };
-  const unsigned grid = (unsigned)std::min<long>(T, (long)sms * 16);
   if (row_bytes % 32 == 0 && all(aligned32))
     return bf16 ? launch_gather_backward<mr::Vec32, true>(dxs, inv_perm, add, dx, T,
-                                                          row_bytes / 32, k, grid, s)
+                                                          row_bytes / 32, k, sms, s)
                 : launch_gather_backward<mr::Vec32, false>(dxs, inv_perm, add, dx, T,
-                                                           row_bytes / 32, k, grid, s);
+                                                           row_bytes / 32, k, sms, s);
   if (row_bytes % 16 == 0 && all(aligned16))
     return bf16 ? launch_gather_backward<uint4, true>(dxs, inv_perm, add, dx, T, row_bytes / 16, k,
-                                                      grid, s)
+                                                      sms, s)
                 : launch_gather_backward<uint4, false>(dxs, inv_perm, add, dx, T, row_bytes / 16,
-                                                       k, grid, s);
-  return bf16 ? launch_gather_backward<uint16_t, true>(dxs, inv_perm, add, dx, T, d, k, grid, s)
-              : launch_gather_backward<float, false>(dxs, inv_perm, add, dx, T, d, k, grid, s);
+                                                       k, sms, s);
+  return bf16 ? launch_gather_backward<uint16_t, true>(dxs, inv_perm, add, dx, T, d, k, sms, s)
+              : launch_gather_backward<float, false>(dxs, inv_perm, add, dx, T, d, k, sms, s);
 }
 
 size_t mr_router_backward_workspace_size(int T, int d, int N_r, int k, int flags) {
@@ -1778,18 +1787,23 @@ int mr_router_backward(const void* x, int x_dtype, const void* W, int W_dtype,
     if (rc != MR_OK) return rc;
   }
   if (dW) {
-    const int n = T * k;
+    const int n = T * k, sh = mr::rb::dw_piece_shift(n, d);
     const bool vec = aligned16(x) && d % (xb ? 8 : 4) == 0;
+    auto launch = [&](auto kernel, long nvec) {
+      return kernel(x, perm, offsets, slot, n, N_r, k, sh, nvec, dW, part, dx != nullptr, s);
+    };
     if (vec)
-      rc = xb ? launch_dw_slots<uint4, true>(x, perm, offsets, slot, n, N_r, k, d / 8, dW, part, dx != nullptr, s)
-              : launch_dw_slots<uint4, false>(x, perm, offsets, slot, n, N_r, k, d / 4, dW, part, dx != nullptr, s);
+      rc = xb ? launch(launch_dw_slots<uint4, true>, d / 8)
+              : launch(launch_dw_slots<uint4, false>, d / 4);
     else
-      rc = xb ? launch_dw_slots<uint16_t, true>(x, perm, offsets, slot, n, N_r, k, d, dW, part, dx != nullptr, s)
-              : launch_dw_slots<float, false>(x, perm, offsets, slot, n, N_r, k, d, dW, part, dx != nullptr, s);
-    // no segment of more than kDwRows rows: nothing to join
-    if (rc != MR_OK || n <= mr::rb::kDwRows) return rc;
-    mr::rb::dw_join_kernel<<<dim3((unsigned)N_r, (unsigned)((d + 1023) / 1024)), 256, 0, s>>>(
-        offsets, n, N_r, d, part, dW);
+      rc = xb ? launch(launch_dw_slots<uint16_t, true>, d)
+              : launch(launch_dw_slots<float, false>, d);
+    // no segment of more than a piece's rows: nothing to join
+    if (rc != MR_OK || n <= 1 << sh) return rc;
+    // one column per thread while the GPU holds the CTAs at once, else four
+    const int cols = (long)N_r * ((d + 255) / 256) <= (long)sms * 8 ? 256 : 1024;
+    const dim3 grid((unsigned)N_r, (unsigned)std::min((d + cols - 1) / cols, 65535));
+    mr::rb::dw_join_kernel<<<grid, 256, 0, s>>>(offsets, n, N_r, d, sh, part, dW);
     return launch_status();
   }
   return MR_OK;

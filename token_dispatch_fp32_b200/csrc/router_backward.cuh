@@ -352,22 +352,39 @@ __global__ void __launch_bounds__(kDxThreads)
 // long segment is spread over many SMs.  Bound by L2: T * k rows of x pass from
 // there to the SMs, 12 TB/s on the full DeepSeek-V3 batch (151 us; pieces of 512
 // rows make the whole call 14 us longer).
-constexpr int kDwRows = 256;
+constexpr int kDwMaxShift = 8;
+constexpr int kDwRows = 1 << kDwMaxShift;  // at most; dw_piece_shift
 constexpr int kDwThreads = 128;
+constexpr int kDwWide = 4;  // columns or words per thread where no 16-byte vector fits
+
+// log2 of the rows of a piece, for n sorted rows of d columns.  A piece is a chain of loads
+// (U rows at a time), so fewer of them than the GPU holds CTAs leave it waiting:
+// halved until there are enough.  Pieces of 256 / 128 / 64 / 32 rows, dW alone:
+// 2048 x 2 rows of 4096 38 / 27 / 19 / 16 us, 1577 x 8 of 1088 44 / 29 / 20 / 18,
+// 4096 x 8 of 7168 on 256 experts 51 / 59 / 60 / 67, 16384 x 8 166 / 171 / 197 /
+// 254 (the partial sums cost more than the balance gains).  Up to 256 rows in
+// all stay one piece per expert, without the launch that joins them.
+inline int dw_piece_shift(long n, long d) {
+  int sh = kDwMaxShift;
+  if (n <= kDwRows) return sh;
+  while (sh > 5 && (n >> sh) * ((d + 1023) / 1024) < 512) --sh;
+  return sh;
+}
 
 // Extra pieces (beyond an expert's first) of all experts before expert e are
-// numbered consecutively; there are at most T*k / kDwRows of them.
+// numbered consecutively; there are at most n >> sh of them (1 << sh rows a piece).
 struct Piece {
   int e, row0, rows, extra;  // extra: index in `part`, -1 for an expert's first piece
 };
 
-__device__ __forceinline__ int pieces(int rows) {
-  return rows > kDwRows ? (rows + kDwRows - 1) / kDwRows : 1;
+// (pieces hold 1 << sh rows)
+__device__ __forceinline__ int pieces(int rows, int sh) {
+  return rows > (1 << sh) ? (rows + (1 << sh) - 1) >> sh : 1;
 }
 
 // Finds piece `b` (all threads of the CTA call it; e = -1 past the last one).
 __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets, int N_r, int n,
-                                            int b) {
+                                            int sh, int b) {
   __shared__ Piece found;
   __shared__ int wsum[2][kDwThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -383,7 +400,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
   int mine = 0, extra = 0;
   for (int e = e0; e < e1; ++e) {
     int lo;
-    const int p = pieces(rows_of(e, lo));
+    const int p = pieces(rows_of(e, lo), sh);
     mine += p;
     extra += p - 1;
   }
@@ -410,15 +427,15 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
   if (b >= before && b < before + mine) {
     for (int e = e0; e < e1; ++e) {
       int lo;
-      const int cnt = rows_of(e, lo), p = pieces(cnt);
+      const int cnt = rows_of(e, lo), p = pieces(cnt, sh);
       if (b < before + p) {
         const int i = b - before;
         found.e = e;
-        found.row0 = lo + i * kDwRows;
-        found.rows = cnt - i * kDwRows < kDwRows ? cnt - i * kDwRows : kDwRows;
+        found.row0 = lo + (i << sh);
+        found.rows = cnt - (i << sh) < (1 << sh) ? cnt - (i << sh) : 1 << sh;
         found.extra = i == 0 ? -1 : xb + i - 1;
         // more extra pieces than `part` holds: offsets that overlap
-        if (found.extra >= n / kDwRows) {
+        if (found.extra >= n >> sh) {
           found.e = -1;
           mr_raise(MR_FLAG_BAD_INDEX);
         }
@@ -432,22 +449,44 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
   return found;
 }
 
-// V: uint4 (8 bf16 or 4 fp32 columns per thread) or one element.
+// V: uint4 (8 bf16 or 4 fp32 columns per thread), or for rows that no vector
+// fits kDwWide columns per thread (float) or words (uint16_t: pairs of bf16).
+//
+// Rows of bf16 at odd addresses are read as whole words all the same.  A row that
+// starts on a word has columns 2w, 2w + 1 in its word w, one that starts inside a
+// word has 2w - 1, 2w there; each kind has sums of its own, which meet at the end
+// (the lower half of the second kind belongs to the word before, so a CTA's last
+// word serves only that one).  With one element per load, 16384 rows of 7105
+// took 864 us.
+template <typename V, bool BF16>
+struct DwShape {
+  static constexpr bool kPairs = sizeof(V) == 2;
+  static constexpr int VU = sizeof(V) == 16 ? 1 : kDwWide;
+  // vectors, columns or words per CTA
+  static constexpr int kSpan = VU * kDwThreads - (kPairs ? 1 : 0);
+  static unsigned slabs(long nvec) {
+    const long units = kPairs ? (nvec + 1) / 2 : nvec;
+    return (unsigned)((units + kSpan - 1) / kSpan);
+  }
+};
+
 template <typename V, bool BF16>
 __global__ void __launch_bounds__(kDwThreads)
     dw_slots_kernel(const V* __restrict__ x, const int32_t* __restrict__ perm,
                     const int32_t* __restrict__ offsets, const float* __restrict__ slot, int n,
-                    int N_r, int k, long nvec, float* __restrict__ dW, float* __restrict__ part,
-                    bool wait_first) {
+                    int N_r, int k, int sh, long nvec, float* __restrict__ dW,
+                    float* __restrict__ part, bool wait_first) {
   using R = RowVec<V, BF16>;
+  using S = DwShape<V, BF16>;
   constexpr int NE = R::kElems;
+  constexpr int VU = S::VU;
   constexpr int U = 8;
   // Programmatic dependent of dlogits_kernel (wait_first), or of dx_slots_kernel,
   // every CTA of which (one wave) has seen dlogits_kernel complete before this
   // kernel starts; then only this kernel's end waits for that one's, so that
   // whatever follows on the stream comes after both.
   if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Piece pc = find_piece(offsets, N_r, n, blockIdx.x);
+  const Piece pc = find_piece(offsets, N_r, n, sh, blockIdx.x);
   if (pc.e < 0) {
     if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -461,53 +500,151 @@ __global__ void __launch_bounds__(kDwThreads)
     tok[i] = ok ? p / k : -1;
     gs[i] = ok ? slot[p] : 0.0f;
   }
+  if constexpr (S::kPairs) {  // whole groups: the piece's first row again, not added
+    const int i = pc.rows + threadIdx.x;
+    if (i < (pc.rows + U - 1) / U * U) {
+      const int p = perm[pc.row0];
+      tok[i] = p >= 0 && p < n ? p / k : -1;
+    }
+  }
   __syncthreads();
-  const long v = (long)blockIdx.y * kDwThreads + threadIdx.x;
-  if (v < nvec) {
-    float acc[NE];
+  const long v0 = (long)blockIdx.y * S::kSpan + threadIdx.x;
+  const long d = nvec * NE;
+  float* out = pc.extra < 0 ? dW + (long)pc.e * d : part + (long)pc.extra * d;
+  if constexpr (S::kPairs) {
+    float even[VU][2], odd[VU][2];
+    bool in[VU];  // a half of this word, or of the row's end, is in the row
 #pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < VU; ++i) {
+      even[i][0] = even[i][1] = odd[i][0] = odd[i][1] = 0.0f;
+      in[i] = 2 * (v0 + i * kDwThreads) <= d;
+    }
+    auto inside = [](const V* row) { return (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1; };
+    const int last = n / k - 1;
     for (int r = 0; r < pc.rows; r += U) {
-      V xv[U];
+      uint32_t xv[U][VU];
+      // The halves a word has outside its row go to sums that no column uses, so
+      // they may be read: all but those of the first and the last row, which
+      // may lie outside x.
+      bool edge = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) edge |= tok[r + u] <= 0 || tok[r + u] >= last;
+      if (!edge) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const V* row = x + (long)tok[r + u] * d;
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(row - inside(row)) + v0;
+#pragma unroll
+          for (int i = 0; i < VU; ++i) xv[u][i] = in[i] ? ld_stream(q + i * kDwThreads) : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int t = tok[r + u];
+          const V* row = x + (long)t * d;
+#pragma unroll
+          for (int i = 0; i < VU; ++i) {
+            const long c = 2 * (v0 + i * kDwThreads) - inside(row);
+            xv[u][i] = 0;
+            if (t >= 0 && c >= 0 && c < d) xv[u][i] = row[c];
+            if (t >= 0 && c + 1 < d) xv[u][i] |= (uint32_t)row[c + 1] << 16;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + u >= pc.rows || tok[r + u] < 0) continue;
+        const float g = gs[r + u];
+        float lo, hi;
+        if (inside(x + (long)tok[r + u] * d)) {
+#pragma unroll
+          for (int i = 0; i < VU; ++i) {
+            bf16x2_unpack(xv[u][i], lo, hi);
+            fma2(odd[i][0], odd[i][1], g, lo, hi);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VU; ++i) {
+            bf16x2_unpack(xv[u][i], lo, hi);
+            fma2(even[i][0], even[i][1], g, lo, hi);
+          }
+        }
+      }
+    }
+    __shared__ float next[VU * kDwThreads];
+#pragma unroll
+    for (int i = 0; i < VU; ++i) next[i * kDwThreads + threadIdx.x] = odd[i][0];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < VU; ++i) {
+      const int l = i * kDwThreads + threadIdx.x;
+      const long c = 2 * (v0 + i * kDwThreads);
+      if (l >= S::kSpan) continue;
+      if (c < d) out[c] = even[i][0] + odd[i][1];
+      if (c + 1 < d) out[c + 1] = even[i][1] + next[l + 1];
+    }
+  } else if (v0 < nvec) {
+    float acc[VU][NE];
+#pragma unroll
+    for (int j = 0; j < VU; ++j)
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[j][i] = 0.0f;
+    for (int r = 0; r < pc.rows; r += U) {
+      V xv[U][VU];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = r + u < pc.rows ? tok[r + u] : -1;
-        xv[u] = t >= 0 ? ld_stream(x + (long)t * nvec + v) : V{};
+#pragma unroll
+        for (int j = 0; j < VU; ++j) {
+          const long v = v0 + j * kDwThreads;
+          xv[u][j] = t >= 0 && (VU == 1 || v < nvec) ? ld_stream(x + (long)t * nvec + v) : V{};
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float g = r + u < pc.rows ? gs[r + u] : 0.0f;
-        float xf[NE];
-        R::unpack(xv[u], xf);
-        if constexpr (NE % 2 == 0) {
 #pragma unroll
-          for (int i = 0; i < NE; i += 2) fma2(acc[i], acc[i + 1], g, xf[i], xf[i + 1]);
-        } else {
-          acc[0] = fmaf(g, xf[0], acc[0]);
+        for (int j = 0; j < VU; ++j) {
+          float xf[NE];
+          R::unpack(xv[u][j], xf);
+          if constexpr (NE % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < NE; i += 2)
+              fma2(acc[j][i], acc[j][i + 1], g, xf[i], xf[i + 1]);
+          } else {
+            acc[j][0] = fmaf(g, xf[0], acc[j][0]);
+          }
         }
       }
     }
-    const long d = nvec * NE;
-    float* out = (pc.extra < 0 ? dW + (long)pc.e * d : part + (long)pc.extra * d) + v * NE;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) out[i] = acc[i];
+    for (int j = 0; j < VU; ++j) {
+      const long v = v0 + j * kDwThreads;
+      if (VU > 1 && v >= nvec) break;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) out[v * NE + i] = acc[j][i];
+    }
   }
   if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // dW[e] += the extra pieces of e, in order.
 __global__ void __launch_bounds__(256)
-    dw_join_kernel(const int32_t* __restrict__ offsets, int n, int N_r, int d,
+    dw_join_kernel(const int32_t* __restrict__ offsets, int n, int N_r, int d, int sh,
                    const float* __restrict__ part, float* __restrict__ dW) {
   const int e = blockIdx.x;
   __shared__ int first_s, count_s;
+  {  // no extra piece: nothing to add
+    const int lo = offsets[e], hi = offsets[e + 1];
+    if ((hi > n ? n : hi) - (lo < 0 ? 0 : lo) <= 1 << sh) return;
+  }
   if (threadIdx.x < 32) {
     int x = 0, mine = 0;
     for (int i = threadIdx.x; i <= e; i += 32) {
       int lo = offsets[i], hi = offsets[i + 1];
       lo = lo < 0 ? 0 : lo;
       hi = hi > n ? n : hi;
-      const int p = pieces(hi - lo);
+      const int p = pieces(hi - lo, sh);
       if (i == e) mine = p;
       else x += p - 1;
     }
@@ -523,10 +660,18 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int first = first_s, count = count_s;
-  if (count <= 1 || first + count - 1 > n / kDwRows) return;
+  if (count <= 1 || first + count - 1 > n >> sh) return;
   for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < d; c += gridDim.y * blockDim.x) {
     float s = dW[(long)e * d + c];
-    for (int i = 0; i + 1 < count; ++i) s += part[(long)(first + i) * d + c];
+    for (int i = 0; i + 1 < count; i += 8) {  // eight loads in flight, added in order
+      float p[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        p[u] = i + u + 1 < count ? part[(long)(first + i + u) * d + c] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u + 1 < count) s += p[u];
+    }
     dW[(long)e * d + c] = s;
   }
 }

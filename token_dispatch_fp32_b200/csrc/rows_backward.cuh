@@ -99,6 +99,16 @@ __host__ __device__ constexpr int bwd_unroll() {
   return sizeof(V) >= 16 ? 1 : 4;
 }
 
+// Rows of up to two vectors per thread of a small CTA go to CTAs of that size:
+// more tokens in flight, fewer idle threads.  combine / gather gradient of 16384
+// x 8 bf16 rows of 1024 118 / 68 us with kRowThreads, 88 / 50 so; 8192 x 6 of 2048
+// 70 / 42 and 68 / 39; 15452 x 2 of 384 47 / 28 and 28 / 22.
+constexpr int kRowSmall = 64;
+template <typename V>
+bool small_rows(long nvec) {
+  return nvec <= 2 * kRowSmall * bwd_unroll<V>();
+}
+
 // Sorted row of slot i of T * k, -1 for none: a dropped slot, or (flagged) an
 // entry past the rows.
 __device__ __forceinline__ long slot_row(const int32_t* inv, long i, long rows) {
@@ -108,8 +118,8 @@ __device__ __forceinline__ long slot_row(const int32_t* inv, long i, long rows) 
 }
 
 // E may be null (no dw wanted), dE may be null (frozen experts).
-template <typename V, bool BF16>
-__global__ void __launch_bounds__(kRowThreads)
+template <typename V, bool BF16, int kThreads>
+__global__ void __launch_bounds__(kThreads)
     combine_backward_kernel(const V* __restrict__ dy, const V* __restrict__ E,
                             const float* __restrict__ w, const int32_t* __restrict__ inv,
                             V* __restrict__ dE, float* __restrict__ dw, long nvec, int k) {
@@ -117,15 +127,15 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int NE = R::kElems;
   constexpr int VU = bwd_unroll<V>();
   constexpr int kBwdGroup = bwd_group<V>();
-  constexpr int kWarps = kRowThreads / 32;
+  constexpr int kWarps = kThreads / 32;
   __shared__ long row_s[kRowMaxK];
   __shared__ float w_s[kRowMaxK];
   __shared__ float red[kWarps][kBwdGroup];
   const long t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < k) {
-    row_s[threadIdx.x] = slot_row(inv, t * k + threadIdx.x, (long)gridDim.x * k);
-    w_s[threadIdx.x] = w[t * k + threadIdx.x];
+  for (int j = threadIdx.x; j < k; j += kThreads) {
+    row_s[j] = slot_row(inv, t * k + j, (long)gridDim.x * k);
+    w_s[j] = w[t * k + j];
   }
   __syncthreads();
   const V* g = dy + t * nvec;
@@ -137,11 +147,11 @@ __global__ void __launch_bounds__(kRowThreads)
       row[u] = j0 + u < k ? row_s[j0 + u] : -1;
       dot[u] = 0.0f;
     }
-    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kRowThreads) {
+    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kThreads) {
       V gv[VU], e[VU][kBwdGroup];
 #pragma unroll
       for (int i = 0; i < VU; ++i) {
-        const long v = v0 + i * kRowThreads;
+        const long v = v0 + i * kThreads;
         const bool in = VU == 1 || v < nvec;
         gv[i] = in ? ld_stream(g + v) : V{};
         if (E) {
@@ -152,7 +162,7 @@ __global__ void __launch_bounds__(kRowThreads)
       }
 #pragma unroll
       for (int i = 0; i < VU; ++i) {
-        const long v = v0 + i * kRowThreads;
+        const long v = v0 + i * kThreads;
         if (VU > 1 && v >= nvec) break;
         float gf[NE];
         R::unpack(gv[i], gf);
@@ -195,8 +205,8 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-template <typename V, bool BF16>
-__global__ void __launch_bounds__(kRowThreads)
+template <typename V, bool BF16, int kThreads>
+__global__ void __launch_bounds__(kThreads)
     gather_backward_kernel(const V* __restrict__ dxs, const int32_t* __restrict__ inv,
                            const V* add, V* dx, long T, long nvec,
                            int k) {
@@ -206,14 +216,14 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int kBwdGroup = bwd_group<V>();
   __shared__ long row_s[kRowMaxK];
   for (long t = blockIdx.x; t < T; t += gridDim.x) {
-    if (threadIdx.x < k) row_s[threadIdx.x] = slot_row(inv, t * k + threadIdx.x, T * k);
+    for (int j = threadIdx.x; j < k; j += kThreads) row_s[j] = slot_row(inv, t * k + j, T * k);
     __syncthreads();
-    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kRowThreads) {
+    for (long v0 = threadIdx.x; v0 < nvec; v0 += VU * kThreads) {
       V av[VU];
       float acc[VU][NE];
 #pragma unroll
       for (int i = 0; i < VU; ++i) {
-        const long v = v0 + i * kRowThreads;
+        const long v = v0 + i * kThreads;
         av[i] = add && v < nvec ? ld_plain(add + t * nvec + v) : V{};
 #pragma unroll
         for (int c = 0; c < NE; ++c) acc[i][c] = 0.0f;
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreads)
           const long r = j0 + u < k ? row_s[j0 + u] : -1;
 #pragma unroll
           for (int i = 0; i < VU; ++i) {
-            const long v = v0 + i * kRowThreads;
+            const long v = v0 + i * kThreads;
             e[i][u] = r >= 0 && v < nvec ? ld_stream(dxs + r * nvec + v) : V{};
           }
         }
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kRowThreads)
       }
 #pragma unroll
       for (int i = 0; i < VU; ++i) {
-        const long v = v0 + i * kRowThreads;
+        const long v = v0 + i * kThreads;
         if (v >= nvec) break;
         if (add) {
           float af[NE];
