@@ -131,6 +131,38 @@ def test_gather_backward_skips_dropped_slots(dtype):
     assert (widen(_host(dx))[1] == 0).all()
 
 
+@pytest.mark.parametrize("d", [1, 2, 3, 509, 510, 511, 1021, 1022, 1023, 1500])
+@pytest.mark.parametrize("off", [0, 1])
+def test_gather_backward_of_rows_inside_words(d, off):
+    """bf16 rows of any width and start, some slots dropped: what lies before
+    and behind dxs and the rows of dropped slots (NaN) stay out of the sums,
+    and nothing outside dx is written."""
+    T, k, N_r = 90, 5, 16
+    rng = np.random.default_rng(d)
+    _, _, _, inv = oracle.dispatch(_ids(rng, T, k, N_r), N_r)
+    dxs, add = _rows(rng, (T * k, d), "bf16"), _rows(rng, (T, d), "bf16")
+    drop = rng.random(T * k) < 0.2
+    drop[inv == 0] = drop[inv == T * k - 1] = False  # the first and the last row are read
+    dxs[inv[drop]] = 0x7FC1
+    inv = np.where(drop, -1, inv).astype(np.int32)
+
+    def inside(a):
+        buf = torch.full((a.size + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        view = buf[8 + off:8 + off + a.size].view(a.shape)
+        view.copy_(_dev(a))
+        return buf, view
+
+    (_, src), (_, plus), (buf, out) = inside(dxs), inside(add), inside(np.zeros_like(add))
+    mr.mr_gather_rows_backward(src, k, _i32(inv), add=plus, dx=out)
+    assert mr.mr_get_error() == mr.MR_OK
+    want, mag = gr.gather_backward(np.where(np.isnan(widen(dxs)), 0, widen(dxs)), inv, k,
+                                   widen(add))
+    gr.check(widen(_host(out.contiguous())), want, (k + 1) * gr.U * mag, "bf16", "dx")
+    assert buf[:8 + off].isnan().all() and buf[8 + off + add.size:].isnan().all()
+    mr.mr_gather_rows_backward(src, k, _i32(inv), add=plus, dx=plus)  # in place
+    assert torch.equal(plus, out)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("off", [16, 4])
 def test_row_gradients_on_unaligned_buffers(dtype, off):

@@ -1446,9 +1446,15 @@ int launch_gather_backward(const void* dxs, const int32_t* inv, const void* add,
         k);
     return launch_status();
   };
-  return mr::small_rows<V>(nvec)
-             ? launch(mr::gather_backward_kernel<V, BF16, mr::kRowSmall>, mr::kRowSmall, 32)
-             : launch(mr::gather_backward_kernel<V, BF16, mr::kRowThreads>, mr::kRowThreads, 16);
+  if constexpr (sizeof(V) == 2) {
+    return mr::small_rows<V>(nvec)
+               ? launch(mr::gather_backward_words_kernel<mr::kRowSmall>, mr::kRowSmall, 32)
+               : launch(mr::gather_backward_words_kernel<mr::kRowThreads>, mr::kRowThreads, 16);
+  } else {
+    return mr::small_rows<V>(nvec)
+               ? launch(mr::gather_backward_kernel<V, BF16, mr::kRowSmall>, mr::kRowSmall, 32)
+               : launch(mr::gather_backward_kernel<V, BF16, mr::kRowThreads>, mr::kRowThreads, 16);
+  }
 }
 
 // Workspace of mr_router_backward: the slots' logit gradients (sigmoid), or

@@ -87,11 +87,14 @@ __global__ void __launch_bounds__(32 * kDlWarps)
     if (lane < k) slot[t * k + lane] = dl;
     if (dense) {
       for (int i = lane; i < N_r; i += 32) dense[t * N_r + i] = 0.0f;
-      __syncwarp();
-      for (int j = 0; j < k; ++j) {  // one after the other: an id may repeat
-        if (lane == j && ok) dense[t * N_r + e] += dl;
-        __syncwarp();
+      float sum = 0.0f;  // an id may repeat: its slots' sum, the same in each of their lanes
+      for (int j = 0; j < k; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j);
+        const float dj = __shfl_sync(0xffffffffu, dl, j);
+        if (ej == e) sum += dj;
       }
+      __syncwarp();
+      if (ok) dense[t * N_r + e] = sum;
     }
   } else {
     float mx = -INFINITY;
@@ -344,25 +347,25 @@ __global__ void __launch_bounds__(kDxThreads)
 
 // ---- sigmoid: dW[e] = sum over the sorted rows r of e of dl[perm[r]] * x[perm[r]/k]
 //
-// Each expert's segment is cut into pieces of kDwRows sorted rows (at least
-// one, so that an expert without rows gets its zeros); a CTA takes one piece
+// Each expert's segment is cut into pieces of 1 << sh sorted rows (at least one
+// piece, so that an expert without rows gets its zeros); a CTA takes one piece
 // and one slab of columns (consecutive CTAs share the slab, so its columns of x
 // stay in L2 while every expert reads them).  An expert's first piece goes to
 // dW, the others to `part`, and dw_join_kernel adds them in order: no atomics, a
 // long segment is spread over many SMs.  Bound by L2: T * k rows of x pass from
-// there to the SMs, 12 TB/s on the full DeepSeek-V3 batch (151 us; pieces of 512
-// rows make the whole call 14 us longer).
+// there to the SMs, 12 TB/s on the full DeepSeek-V3 batch (the call 314 us of GPU
+// time, of which dx 150; pieces of 512 rows make it 14 us longer).
 constexpr int kDwMaxShift = 8;
 constexpr int kDwRows = 1 << kDwMaxShift;  // at most; dw_piece_shift
 constexpr int kDwThreads = 128;
 constexpr int kDwWide = 4;  // columns or words per thread where no 16-byte vector fits
 
-// log2 of the rows of a piece, for n sorted rows of d columns.  A piece is a chain of loads
-// (U rows at a time), so fewer of them than the GPU holds CTAs leave it waiting:
-// halved until there are enough.  Pieces of 256 / 128 / 64 / 32 rows, dW alone:
-// 2048 x 2 rows of 4096 38 / 27 / 19 / 16 us, 1577 x 8 of 1088 44 / 29 / 20 / 18,
-// 4096 x 8 of 7168 on 256 experts 51 / 59 / 60 / 67, 16384 x 8 166 / 171 / 197 /
-// 254 (the partial sums cost more than the balance gains).  Up to 256 rows in
+// log2 of the rows of a piece, for n sorted rows of d columns.  A piece is a
+// chain of loads (eight rows at a time), so fewer of them than the GPU holds CTAs
+// leave it waiting: halved until there are 512.  Pieces of 256 / 128 / 64 / 32
+// rows, dW alone: 2048 x 2 rows of 4096 38 / 27 / 19 / 16 us, 1577 x 8 of 1088
+// 44 / 29 / 20 / 18, 4096 x 8 of 7168 on 256 experts 51 / 59 / 60 / 67, 16384 x 8
+// 166 / 171 / 197 / 254 (the partial sums cost more than the balance gains).  Up to 256 rows in
 // all stay one piece per expert, without the launch that joins them.
 inline int dw_piece_shift(long n, long d) {
   int sh = kDwMaxShift;
@@ -461,6 +464,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
 template <typename V, bool BF16>
 struct DwShape {
   static constexpr bool kPairs = sizeof(V) == 2;
+  static constexpr int kElems = (int)sizeof(V) / (BF16 ? 2 : 4);  // columns of a V
   static constexpr int VU = sizeof(V) == 16 ? 1 : kDwWide;
   // vectors, columns or words per CTA
   static constexpr int kSpan = VU * kDwThreads - (kPairs ? 1 : 0);
@@ -476,9 +480,8 @@ __global__ void __launch_bounds__(kDwThreads)
                     const int32_t* __restrict__ offsets, const float* __restrict__ slot, int n,
                     int N_r, int k, int sh, long nvec, float* __restrict__ dW,
                     float* __restrict__ part, bool wait_first) {
-  using R = RowVec<V, BF16>;
   using S = DwShape<V, BF16>;
-  constexpr int NE = R::kElems;
+  constexpr int NE = S::kElems;
   constexpr int VU = S::VU;
   constexpr int U = 8;
   // Programmatic dependent of dlogits_kernel (wait_first), or of dx_slots_kernel,
@@ -519,7 +522,6 @@ __global__ void __launch_bounds__(kDwThreads)
       even[i][0] = even[i][1] = odd[i][0] = odd[i][1] = 0.0f;
       in[i] = 2 * (v0 + i * kDwThreads) <= d;
     }
-    auto inside = [](const V* row) { return (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1; };
     const int last = n / k - 1;
     for (int r = 0; r < pc.rows; r += U) {
       uint32_t xv[U][VU];
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kDwThreads)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const V* row = x + (long)tok[r + u] * d;
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(row - inside(row)) + v0;
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(row - starts_inside(row)) + v0;
 #pragma unroll
           for (int i = 0; i < VU; ++i) xv[u][i] = in[i] ? ld_stream(q + i * kDwThreads) : 0u;
         }
@@ -544,10 +546,8 @@ __global__ void __launch_bounds__(kDwThreads)
           const V* row = x + (long)t * d;
 #pragma unroll
           for (int i = 0; i < VU; ++i) {
-            const long c = 2 * (v0 + i * kDwThreads) - inside(row);
-            xv[u][i] = 0;
-            if (t >= 0 && c >= 0 && c < d) xv[u][i] = row[c];
-            if (t >= 0 && c + 1 < d) xv[u][i] |= (uint32_t)row[c + 1] << 16;
+            const long c = 2 * (v0 + i * kDwThreads) - starts_inside(row);
+            xv[u][i] = t >= 0 ? two_elements(row, c, d) : 0u;
           }
         }
       }
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kDwThreads)
         if (r + u >= pc.rows || tok[r + u] < 0) continue;
         const float g = gs[r + u];
         float lo, hi;
-        if (inside(x + (long)tok[r + u] * d)) {
+        if (starts_inside(x + (long)tok[r + u] * d)) {
 #pragma unroll
           for (int i = 0; i < VU; ++i) {
             bf16x2_unpack(xv[u][i], lo, hi);
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kDwThreads)
 #pragma unroll
         for (int j = 0; j < VU; ++j) {
           float xf[NE];
-          R::unpack(xv[u][j], xf);
+          RowVec<V, BF16>::unpack(xv[u][j], xf);
           if constexpr (NE % 2 == 0) {
 #pragma unroll
             for (int i = 0; i < NE; i += 2)

@@ -92,8 +92,7 @@ __host__ __device__ constexpr int bwd_group() {
 }
 
 // Vectors of a row in flight per thread and slot: one 16- or 32-byte vector,
-// four single elements (with one, the element path of 1999 tokens x 3 slots of
-// 1001 bf16 took 23.6 us, a chain of load latencies).
+// four single elements (one would be a chain of load latencies).
 template <typename V>
 __host__ __device__ constexpr int bwd_unroll() {
   return sizeof(V) >= 16 ? 1 : 4;
@@ -263,6 +262,126 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncthreads();
+  }
+}
+
+// ---- gather: rows of bf16 that no vector fits -----------------------------------
+//
+// Read as whole words all the same.  A row that starts on a word has columns
+// 2w, 2w + 1 in its word w, one that starts inside a word (o = 1) has 2w - 1, 2w
+// there.  The first and the last row are read by elements: their outer words may
+// lie outside the buffer.  8192 x 6 rows of 2049 take 81 us, 137 by elements.
+// combine's gradient keeps to elements (142 us): by words it needs dy at both
+// offsets and writes rows of either kind too, and took 200 to 340 us.
+constexpr int kWordUnroll = 4, kWordGroup = 4;
+
+__device__ __forceinline__ int starts_inside(const uint16_t* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+}
+// Columns c, c + 1 of a row of d by elements, 0 outside.
+__device__ __forceinline__ uint32_t two_elements(const uint16_t* row, long c, long d) {
+  uint32_t v = 0;
+  if (c >= 0 && c < d) v = row[c];
+  if (c + 1 >= 0 && c + 1 < d) v |= (uint32_t)row[c + 1] << 16;
+  return v;
+}
+
+// Rows of either kind have sums of their own, which meet at the end: the lower
+// half of the second kind belongs to the word before, so the last word of a
+// span serves only that one.  A half outside the row goes to a sum that no
+// column uses.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    gather_backward_words_kernel(const uint16_t* __restrict__ dxs,
+                                 const int32_t* __restrict__ inv, const uint16_t* add,
+                                 uint16_t* dx, long T, long d, int k) {
+  constexpr int VU = kWordUnroll, G = kWordGroup;
+  constexpr int kSpan = VU * kThreads - 1;
+  __shared__ long row_s[kRowMaxK];
+  __shared__ float next[VU * kThreads];
+  for (long t = blockIdx.x; t < T; t += gridDim.x) {
+    for (int j = threadIdx.x; j < k; j += kThreads) row_s[j] = slot_row(inv, t * k + j, T * k);
+    __syncthreads();
+    for (long base = 0; base < (d + 1) / 2; base += kSpan) {
+      const long w0 = base + threadIdx.x;
+      float even[VU][2], odd[VU][2], av[VU][2];
+      bool in[VU];  // a half of this word, or of the row's end, is in the row
+#pragma unroll
+      for (int i = 0; i < VU; ++i) {
+        const long c = 2 * (w0 + i * kThreads);
+        even[i][0] = even[i][1] = odd[i][0] = odd[i][1] = 0.0f;
+        in[i] = c <= d;
+        av[i][0] = add && c < d ? mr_bf16_to_f32(ld_plain(add + t * d + c)) : 0.0f;
+        av[i][1] = add && c + 1 < d ? mr_bf16_to_f32(ld_plain(add + t * d + c + 1)) : 0.0f;
+      }
+      for (int j0 = 0; j0 < k; j0 += G) {
+        uint32_t x[G][VU];
+        long row[G];
+        bool edge = false;
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          row[u] = j0 + u < k ? row_s[j0 + u] : -1;
+          edge |= row[u] == 0 || row[u] == T * k - 1;
+        }
+        if (!edge) {
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            const uint16_t* r = dxs + row[u] * d;
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(r - starts_inside(r)) + w0;
+#pragma unroll
+            for (int i = 0; i < VU; ++i)
+              x[u][i] = row[u] >= 0 && in[i] ? ld_stream(q + i * kThreads) : 0u;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            const uint16_t* r = dxs + row[u] * d;
+#pragma unroll
+            for (int i = 0; i < VU; ++i)
+              x[u][i] = row[u] >= 0
+                            ? two_elements(r, 2 * (w0 + i * kThreads) - starts_inside(r), d)
+                            : 0u;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+          if (row[u] < 0) continue;
+          const bool o = starts_inside(dxs + row[u] * d);
+#pragma unroll
+          for (int i = 0; i < VU; ++i) {
+            float lo, hi;
+            bf16x2_unpack(x[u][i], lo, hi);
+            if (o) {
+              odd[i][0] += lo;
+              odd[i][1] += hi;
+            } else {
+              even[i][0] += lo;
+              even[i][1] += hi;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VU; ++i) next[i * kThreads + threadIdx.x] = odd[i][0];
+      __syncthreads();
+      const bool inside = starts_inside(dx + t * d);
+#pragma unroll
+      for (int i = 0; i < VU; ++i) {
+        const int l = i * kThreads + threadIdx.x;
+        const long c = 2 * (w0 + i * kThreads);
+        if (l >= kSpan || c >= d) continue;
+        uint16_t* out = dx + t * d + c;
+        const uint32_t v = bf16x2_pack_rn(even[i][0] + odd[i][1] + av[i][0],
+                                          even[i][1] + next[l + 1] + av[i][1]);
+        if (!inside && c + 1 < d) {
+          st_stream(reinterpret_cast<uint32_t*>(out), v);
+        } else {
+          out[0] = (uint16_t)v;
+          if (c + 1 < d) out[1] = (uint16_t)(v >> 16);
+        }
+      }
+      __syncthreads();
+    }
   }
 }
 
