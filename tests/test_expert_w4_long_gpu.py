@@ -1,0 +1,33 @@
+"""The expert layer on 4-bit weights where segments are long or the layer is
+wide: the kernel for many rows, and the choice between the two kernels."""
+import numpy as np
+import pytest
+import torch
+
+import gradients as gr
+import oracle
+import token_dispatch_fp32_b200 as mr
+from parity import widen
+from test_backward_gpu import _f32, _i32, _ids, _rows
+from test_expert_w4_gpu import _problem
+from test_rows_gpu import _dev, _host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n_out", [1001, 2056, 2079])
+def test_columns_do_not_depend_on_the_width(n_out):
+    """150 rows on each of eight experts: the last warp's lanes store only some
+    columns, and every column is the one that a layer of whole warps has."""
+    T, k, N_r, d, group = 200, 6, 8, 264, 32
+    full = -(-n_out // 32) * 32
+    x, perm, offsets, _, q, s = _problem(T, k, N_r, full, d, group, "f32", n_out)
+
+    def layer(n):
+        W4 = mr.mr_expert_pack_w4(torch.from_numpy(q[:, :n].copy()).cuda(),
+                                  _dev(s[:, :n].copy()), group)
+        return mr.mr_expert_gemv_gather_w4(_dev(x), k, _i32(perm), _i32(offsets), W4, N_r, n,
+                                           group, scale_dtype=torch.float32)
+
+    part, whole = layer(n_out), layer(full)
+    assert torch.equal(part.view(torch.int16), whole[:, :n_out].contiguous().view(torch.int16))

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ncols = P.n_out - n0 < kBN ? P.n_out - n0 : kBN;
       for (int c = 0; c < kBN / 16; ++c) {
         float v[16];
+        __syncwarp();
         tmem_ld16(tmem_base + lane_off + (uint32_t)(c * 16), v);  // whole warp
         if (store && c * 16 < ncols) {
 #pragma unroll
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* dst = COMBINE ? nullptr : P.out + (long)j * P.n_out + n0;
     for (int c = 0; c < (COMBINE ? 0 : kBN / 16); ++c) {
       float v[16];
+      __syncwarp();
       tmem_ld16(tmem_base + lane_off + (uint32_t)(c * 16), v);  // whole warp
       if (store && n0 + c * 16 < P.n_out) {
         uint4 pk[2];

@@ -325,14 +325,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       const int col = out0 + q * 32 + lane;
       for (int c0 = 0; c0 < rows; c0 += 16) {
         float v[16];
+        __syncwarp();
         tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);  // whole warp
-        if (!ok || col >= P.n_out) continue;
+        if (ok && col < P.n_out) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (c0 + i >= rows) break;
-          const __nv_bfloat16 b = __float2bfloat16_rn(v[i]);
-          P.out[(long)(row0 + c0 + i) * P.n_out + col] =
-              *reinterpret_cast<const uint16_t*>(&b);
+          for (int i = 0; i < 16; ++i) {
+            if (c0 + i >= rows) break;
+            const __nv_bfloat16 b = __float2bfloat16_rn(v[i]);
+            P.out[(long)(row0 + c0 + i) * P.n_out + col] =
+                *reinterpret_cast<const uint16_t*>(&b);
+          }
         }
       }
     } else {

@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float v[16];
     const int nc = NT / 16, ch = (nc + 1) / 2;
     for (int c = hf * ch; c < nc && c < (hf + 1) * ch; ++c) {
+      __syncwarp();
       tmem_ld16(tmem_base + lane_off + (uint32_t)(c * 16), v);  // whole warp
       if (CL > 1) {
 #pragma unroll
