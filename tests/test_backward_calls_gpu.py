@@ -1,0 +1,37 @@
+"""The gradients as a training loop calls them: one call after another on the
+same buffers."""
+import pytest
+import torch
+
+import oracle
+import token_dispatch_fp32_b200 as mr
+from test_backward_gpu import _f32, _gate_problem, _i32
+from test_rows_gpu import _dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,d,want_dx", [(700, 1024, True), (700, 1024, False),
+                                         (4000, 264, True)])
+def test_gate_gradients_in_a_row_on_one_workspace(T, d, want_dx):
+    """The kernels behind the logit gradients start while those are written:
+    calls that take turns on one workspace read the values of their own call."""
+    N_r, k = 64, 4
+    _, x, W, L, idx, g = _gate_problem(T, d, N_r, k, "bf16", "f32", 0, seed=T)
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    grads = [_f32(g), _f32(-3 * g[::-1])]
+    args = (_dev(x), _dev(W), _f32(L), _i32(idx))
+    plan = (_i32(perm), _i32(offsets), 2.5)
+    ws = torch.empty(mr.mr_router_backward_workspace_size(T, d, N_r, k), dtype=torch.uint8,
+                     device="cuda")
+    ref = []
+    for dw in grads:
+        ref.append(mr.mr_router_backward(*args, dw, *plan, want_dx=want_dx))
+        torch.cuda.synchronize()
+    got = [mr.mr_router_backward(*args, grads[i % 2], *plan, want_dx=want_dx, workspace=ws)
+           for i in range(20)]
+    torch.cuda.synchronize()
+    assert mr.mr_get_error() == mr.MR_OK
+    for i, (dx, dW) in enumerate(got):
+        assert torch.equal(dW, ref[i % 2][1])
+        assert dx is None or torch.equal(dx, ref[i % 2][0])

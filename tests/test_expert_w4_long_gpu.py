@@ -1,16 +1,12 @@
 """The expert layer on 4-bit weights where segments are long or the layer is
 wide: the kernel for many rows, and the choice between the two kernels."""
-import numpy as np
 import pytest
 import torch
 
-import gradients as gr
-import oracle
 import token_dispatch_fp32_b200 as mr
-from parity import widen
-from test_backward_gpu import _f32, _i32, _ids, _rows
+from test_backward_gpu import _i32
 from test_expert_w4_gpu import _problem
-from test_rows_gpu import _dev, _host
+from test_rows_gpu import _dev
 
 pytestmark = pytest.mark.gpu
 

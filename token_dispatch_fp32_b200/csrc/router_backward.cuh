@@ -142,6 +142,8 @@ __global__ void __launch_bounds__(32 * kDlWarps)
 // twice.  A warp takes kDxTokens tokens at a time (independent reads in flight)
 // and stages their (row, dl) pairs in its own piece of shared memory, the next
 // tokens' already on their way (addv may be dxv: neither is __restrict__).
+// slot is not __restrict__ here nor in dw_slots_kernel: dlogits_kernel may still
+// be writing it when these start, so it is read by ordinary loads behind the wait.
 //
 // The kernel is a programmatic dependent of dlogits_kernel: W is loaded while
 // that runs.  Measured on the full DeepSeek-V3 batch (16384 tokens, 256
@@ -165,7 +167,7 @@ __host__ __device__ constexpr size_t dx_smem_bytes(int N_r, int cw, int k) {
 template <int CPL, bool VEC, bool BF16, int kRegs>
 __global__ void __launch_bounds__(kDxThreads)
     dx_slots_kernel(const void* __restrict__ Wv, bool wbf16, const int32_t* __restrict__ idx,
-                    const float* __restrict__ slot, const void* addv, void* dxv, int T, int d,
+                    const float* slot, const void* addv, void* dxv, int T, int d,
                     int N_r, int k) {
   constexpr int CW = 32 * CPL;
   constexpr int U = kDxTokens;
@@ -477,7 +479,7 @@ struct DwShape {
 template <typename V, bool BF16>
 __global__ void __launch_bounds__(kDwThreads)
     dw_slots_kernel(const V* __restrict__ x, const int32_t* __restrict__ perm,
-                    const int32_t* __restrict__ offsets, const float* __restrict__ slot, int n,
+                    const int32_t* __restrict__ offsets, const float* slot, int n,
                     int N_r, int k, int sh, long nvec, float* __restrict__ dW,
                     float* __restrict__ part, bool wait_first) {
   using S = DwShape<V, BF16>;
