@@ -1932,8 +1932,10 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   // rows of x per pass over an expert's weights
   const long n = (long)T * k;
   P.xr = mr::w4::kRowsPerPass;
-  // the most passes that long segments can have (mr::w4::long_to_tile)
-  const long long_passes = n / 16 + n / (mr::w4::kLongRows + 1);
+  // the most passes that long segments can have (mr::w4::long_to_tile); none
+  // where not even all rows make one
+  const long long_passes =
+      n > mr::w4::kLongRows ? n / 16 + n / (mr::w4::kLongRows + 1) : 0;
   P.tile_rows = long_passes * l.tiles > 1000 ? mr::w4::kLongRows : 0;
   P.sms = sms;
   const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
