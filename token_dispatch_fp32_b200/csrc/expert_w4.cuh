@@ -239,15 +239,19 @@ __device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const ui
 // Whether the segments of more than kLongRows rows go to the many-row kernel
 // (expert_w4_tile.cuh), decided alike by both kernels from the segments:
 // `passes` passes of 16 of their rows here, or `blocks` blocks there.  There a
-// 128-row tile of n_out takes an SM 0.6 us for 64 columns, however few the
-// blocks; here a unit and pass takes the whole GPU about 1.4 ns.  Measured (d =
-// 7168, n_out = 2048), here / there: 1 x 128 rows 32 / 96 us, 8 x 48 rows 88 / 84,
-// 8 x 128 rows 150 / 90, 256 x 128 rows 3.7 / 2.3 ms.
+// 128-row tile of n_out takes an SM 1.0 to 1.4 us for 128 columns, however few the
+// rows of its block; here a unit and pass takes the whole GPU 1.4 to 2 ns.
+// Measured (d = 7168, n_out = 2048, groups of 32, bf16 scales), here / there: 4 x 64
+// rows (512 units and passes per wave of items) 64 / 71 us, 8 x 33 rows (768) 89 / 71,
+// 32 x 40 rows (768) 248 / 245, 64 x 40 rows (878) 456 / 419, 4 x 128 rows (1024) 113 /
+// 89, 256 x 128 rows 4.9 / 2.2 ms; groups of 128 with fp32 scales, 8 x 48 rows 87 / 71;
+// d = 1408, n_out = 512, 40 x 64 rows (640) 53 / 42.
 constexpr int kLongRows = 32;
-constexpr int kTileRows = 192;  // rows per block there
+constexpr int kTileRows = 128;     // rows per block there
+constexpr int kTilePasses = 700;   // units and passes that take as long as a wave there
 __device__ __forceinline__ bool long_to_tile(long passes, long blocks, int n_out, int sms) {
   const long items = blocks * ((n_out + 127) / 128);
-  return passes * ((n_out + kTile - 1) / kTile) > 1000 * ((items + sms - 1) / sms);
+  return passes * ((n_out + kTile - 1) / kTile) > kTilePasses * ((items + sms - 1) / sms);
 }
 // The sums over the CTA's threads of (passes, blocks) of their long segments
 // (every thread calls it; tmp: two ints per warp).

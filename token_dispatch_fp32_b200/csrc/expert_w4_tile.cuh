@@ -3,40 +3,43 @@
 // layout).
 //
 // With more rows per expert the widening of the weights is worth sharing: here
-// a CTA widens 128 output rows x 64 columns at a time into shared memory and
-// tcgen05 multiplies them with up to 192 of the expert's rows.  The group scale
-// is applied to the weight, without loss: a bf16 scale (8 significant bits)
-// times an integer in [-8, 7] has at most 12, so the product is the sum of two
-// bf16 planes, hi = bf16(s q) and lo = s q - hi (one multiply and one fused
-// multiply-add per pair); with fp32 scales the fp32 product is split into three.
-// Each plane times bf16 x is exact in fp32, the tensor core adds in fp32, and
-// the result is rounded to bf16 once.
+// a CTA widens 128 output rows x 128 columns at a time into shared memory and
+// tcgen05 multiplies them with up to 128 of the expert's rows.  Each group of
+// columns has an accumulation of its own: u - 8 is exact in bf16 and so is its
+// product with x in fp32, the tensor core adds a group's 2 to 8 steps of 16
+// products (rounding toward zero), and the group's sum, times the scale of its
+// output row, is added to fp32 registers (to nearest); the result is rounded to
+// bf16 once.  One accumulation over all of d, with the scales multiplied into the
+// weights, drifts toward zero with every step: 150 rows x 8 experts (d = 1408)
+// differed by 1.5e-4 (2-norm of the bf16 results) from fp32 sums, 6e-5 so.
 //
-// tcgen05 kind::f16, M = 128 (output rows), N = 16 .. 192 (rows of x, rounded up
-// to 16), K staged 64 at a time (128-byte swizzled rows).  The rows of x and the
-// widened weights have rings of their own.
+// tcgen05 kind::f16, M = 128 (output rows), N = 16 .. 128 (rows of x, rounded up
+// to 16), stages of 128 columns (two halves of 128-byte swizzled rows), TMEM holds
+// four accumulations; groups of 32 and 64 are handed over two at a time (each wait
+// costs the threads that take turns about 150 cycles).
 //   warp 0       TMEM owner and MMA issuer (one elected thread)
-//   warps 1-4    rows of x, 16 bytes a copy (cp.async); at the end TMEM -> bf16
-//                -> out
-//   warps 5-20   weights: two sets of eight warps take the stages in turn; each
-//                lane widens 4 x 8 weights, the words and scales of its set's
-//                next three stages already on their way
-// An item is a block of up to 192 rows of a segment of more than kMinRows rows
+//   warp 1       packed units into a ring (bulk copies)
+//   warps 2-3    rows of x, 16 bytes a copy (cp.async)
+//   warps 4-7    weights: each lane widens 16 x 8 of a stage
+//   warps 8-15   the groups' sums, 32 output rows and up to four times 16 rows of
+//                x each; at the end -> bf16 -> out.  A lane is an output row, so a
+//                group's scale is one register.
+// An item is a block of up to 128 rows of a segment of more than kMinRows rows
 // and a 128-row tile of n_out (none when long_to_tile says that the few-row
 // kernel is faster); one CTA per SM takes items blockIdx.x, + gridDim.x,
 // .. (only the device knows how many there are).  Every mbarrier wait is bounded.
 //
-// Shared memory bounds it: at 128 rows a stage writes 32 KB of widened weights
-// (two planes) and 16 KB of x, and its MMAs read 64 KB, about 900 of the 1150
-// cycles it takes; the widening itself is hidden (sixteen warps).  One block for
-// a segment where blocks of 128 rows would widen its weights twice.  Measured:
-// 150 rows x 8 experts (d = 1408, n_out = 2056, fp32 scales) 67 us with blocks of
-// 128 rows, eight warps and a CTA for every block there might be, 37 us so; 128
-// rows x 256 experts (d = 7168, n_out = 2048) 2.6 ms with the rows' addresses
-// formed for every copy, 2.3 ms so; eight or twelve copy warps 2.4 and 2.6 ms.
+// Measured (d = 7168, n_out = 2048): 128 rows x 256 experts 2.16 ms with groups of
+// 32 (2.28 with scaled weights in two planes and one accumulation), 1.71 with
+// groups of 128 (2.28); 150 rows x 8 experts (d = 1408, n_out = 2056, groups of 128,
+// fp32 scales: three planes before) 32.8 us (36.9); 192 rows x 8 experts, two blocks
+// each here, 152 us (109 with blocks of 192 rows, whose sums do not fit the
+// registers).  With groups of 32 a stage of 128 columns takes about 2200 cycles, of
+// which reading the four sums from TMEM 1730; with groups of 128 about 1600, bound
+// by the two warps that copy x (1180 to issue, 250 for the copies to land); its
+// MMAs take 600.  Sixteen warps for the sums were 1 to 7 % slower, loads of 32
+// columns 10 %.
 #pragma once
-
-#include <type_traits>
 
 #include "expert_w4.cuh"
 
@@ -45,24 +48,23 @@ namespace w4t {
 
 using namespace mr::tc;
 
-constexpr int kRows = w4::kTileRows;  // 192 rows of x per CTA (MMA N at most)
-constexpr int kTmem = 256;       // columns allocated (a power of two)
-constexpr int kOut = 128;        // output rows per CTA (MMA M): two packed units
-constexpr int kK = 64;           // columns per stage
-constexpr int kXStages = 5;      // stages of x
-constexpr int kCopyWarps = 4, kWidenWarps = 8, kWidenSets = 2;
-constexpr int kThreads = 32 * (1 + kCopyWarps + kWidenSets * kWidenWarps);
-constexpr uint32_t kPlane = kOut * kK * 2;
-constexpr uint32_t kXBytes = kRows * kK * 2;
+constexpr int kRows = w4::kTileRows;  // 128 rows of x per CTA (MMA N at most)
+constexpr int kAccs = 4;              // accumulations in TMEM
+constexpr int kTmem = kAccs * kRows;  // columns allocated (a power of two)
+constexpr int kOut = 128;             // output rows per CTA (MMA M): two packed units
+constexpr int kK = 64;                // columns of a 128-byte row
+// Rings of stages of 128 columns (a packed unit): rows of x and widened weights,
+// packed units (two per stage).
+constexpr int kStages = 3, kUnitStages = 3;
+constexpr int kCopyWarps = 2, kWidenWarps = 4, kSumWarps = 8;
+constexpr int kThreads = 32 * (2 + kCopyWarps + kWidenWarps + kSumWarps);
+constexpr uint32_t kWHalf = kOut * kK * 2, kWBytes = 2 * kWHalf;
+constexpr uint32_t kXHalf = kRows * kK * 2, kXBytes = 2 * kXHalf;
+inline uint32_t smem_bytes(int unit_bytes) {
+  return kStages * (kXBytes + kWBytes) + kUnitStages * 2 * (uint32_t)unit_bytes + 1024;
+}
 // Segments of up to this many rows go to the few-row kernel in any case.
 constexpr int kMinRows = w4::kLongRows;
-
-// Stages of widened weights: what the x ring leaves, three of two planes or two
-// of three.
-__host__ __device__ constexpr int w_stages(int planes) { return planes == 2 ? 3 : 2; }
-__host__ __device__ constexpr uint32_t smem_bytes(int planes) {
-  return kXStages * kXBytes + w_stages(planes) * planes * kPlane + 1024;
-}
 
 struct Params {
   const uint16_t* x;
@@ -74,59 +76,42 @@ struct Params {
 };
 
 // Place in a ring of N stages and its parity, from the count g of stages before;
-// kept incrementally (divisions in every warp and stage cost as much as the
-// widening).
+// kept incrementally (divisions in every warp and stage would cost more than
+// they look).
 template <int N>
 struct Place {
   int s;
   uint32_t ph;
   __device__ __forceinline__ explicit Place(int g) : s(g % N), ph((uint32_t)(g / N) & 1u) {}
-  __device__ __forceinline__ void step(int by = 1) {
-    s += by;
-    if (s >= N) {
-      s -= N;
+  __device__ __forceinline__ void step() {
+    if (++s == N) {
+      s = 0;
       ph ^= 1u;
     }
   }
 };
 
-// (u - 8) of the weight pair p of w as two bf16 values.
-__device__ __forceinline__ __nv_bfloat162 weight2(uint32_t w, int p) {
+// u - 8 of the weight pair p of w as two bf16 values.
+__device__ __forceinline__ uint32_t weight2(uint32_t w, int p) {
   const uint32_t v = w4::widen2(w, p);  // 16 + u
   const uint32_t k24 = 0x41c041c0u;
-  return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                 *reinterpret_cast<const __nv_bfloat162*>(&k24));
-}
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
-  return *reinterpret_cast<uint32_t*>(&v);
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&k24));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Planes of s times a weight pair.
-__device__ __forceinline__ void planes2(__nv_bfloat162 q, uint16_t s, uint32_t (&o)[2]) {
-  const uint32_t d = (uint32_t)s | ((uint32_t)s << 16);
-  const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&d);
-  const __nv_bfloat162 hi = __hmul2(q, s2);
-  o[0] = bits(hi);
-  o[1] = bits(__hfma2(q, s2, __hneg2(hi)));
-}
-__device__ __forceinline__ void planes2(__nv_bfloat162 q, float s, uint32_t (&o)[3]) {
-  const uint32_t u = bits(q);
-  float a = s * __uint_as_float(u << 16), b = s * __uint_as_float(u & 0xffff0000u);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {  // pairs at a time: packed conversions
-    o[i] = bits(__floats2bfloat162_rn(a, b));
-    a -= __uint_as_float(o[i] << 16);
-    b -= __uint_as_float(o[i] & 0xffff0000u);
-  }
-}
+__device__ __forceinline__ float to_f32(uint16_t s) { return mr_bf16_to_f32(s); }
+__device__ __forceinline__ float to_f32(float s) { return s; }
 
 template <int GROUP, typename S>
 __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Params P) {
-  constexpr int NP = sizeof(S) == 2 ? 2 : 3;
-  constexpr int kWStages = w_stages(NP);
+  constexpr int kUnitGroups = w4::kCols / GROUP;
+  // accumulations handed over at once, such turns per stage, turns that TMEM holds
+  constexpr int kBatch = GROUP == w4::kCols ? 1 : 2;
+  constexpr int kTurns = kUnitGroups / kBatch, kParts = kAccs / kBatch;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t bars[2 * kXStages + 2 * kWStages + 1];
+  __shared__ uint64_t bars[2 * (kStages + kUnitStages + kParts) + 1];
   __shared__ int tok_s[kRows];
   __shared__ int wsum[kThreads / 32], pair[2 * (kThreads / 32)];
   __shared__ int found[3];
@@ -137,9 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
   const int n = P.T * P.k;
   const uint32_t smem0 = smem_u32(smem);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  const int B_XFULL = 0, B_XEMPTY = kXStages, B_WFULL = 2 * kXStages,
-            B_WEMPTY = 2 * kXStages + kWStages, B_ACC = 2 * kXStages + 2 * kWStages;
-  const uint32_t x0 = smem0, w0 = smem0 + kXStages * kXBytes;  // the rings
+  const int B_FULL = 0, B_EMPTY = kStages, B_ACCF = 2 * kStages, B_ACCE = B_ACCF + kParts,
+            B_UFULL = B_ACCE + kParts, B_UEMPTY = B_UFULL + kUnitStages,
+            B_DRAIN = B_UEMPTY + kUnitStages;
+  // the rings: rows of x, widened weights, packed units (two per 128 columns)
+  constexpr uint32_t kWAt = kStages * kXBytes, kUAt = kWAt + kStages * kWBytes;
+  const uint32_t x0 = smem0, w0 = smem0 + kWAt, u0 = smem0 + kUAt;
 
   // ---- which segment and which block of it ---------------------------------------
   auto segment = [&](int e, int& a) {
@@ -185,17 +173,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     return;  // every thread leaves together
   }
-  const int KC = (P.d + kK - 1) / kK;
+  const int KB = P.KB;  // stages per item
   if (tid == 0) {
-    for (int s = 0; s < kXStages; ++s) {
-      mbar_init(bar(B_XFULL + s), kCopyWarps);
-      mbar_init(bar(B_XEMPTY + s), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(B_FULL + s), 2 * kCopyWarps + kWidenWarps);
+      mbar_init(bar(B_EMPTY + s), 1);
     }
-    for (int s = 0; s < kWStages; ++s) {
-      mbar_init(bar(B_WFULL + s), kWidenWarps);
-      mbar_init(bar(B_WEMPTY + s), 1);
+    for (int b = 0; b < kParts; ++b) {
+      mbar_init(bar(B_ACCF + b), 1);
+      mbar_init(bar(B_ACCE + b), kSumWarps);
     }
-    mbar_init(bar(B_ACC), 1);
+    for (int s = 0; s < kUnitStages; ++s) {
+      mbar_init(bar(B_UFULL + s), 1);
+      mbar_init(bar(B_UEMPTY + s), kWidenWarps + kSumWarps);
+    }
+    mbar_init(bar(B_DRAIN), 1);
     abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -243,69 +235,100 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       tok_s[tid] = tok;
     }
     __syncthreads();
-    const int g0 = done * KC;  // stages before this item's
+    const int g0 = done * KB;  // stages and pairs of units before this item's
+    const int tile = out0 / w4::kTile;
+    const int tiles_here = min(2, P.tiles - tile);
 
     if (warp == 0) {
       if (lane == 0) {
         const uint32_t idesc = make_idesc_bf16((rows + 15) / 16 * 16, kOut);
-        Place<kXStages> xp(g0);
-        Place<kWStages> wp(g0);
-        for (int kc = 0; kc < KC; ++kc, xp.step(), wp.step()) {
-          if (!mbar_wait(bar(B_XFULL + xp.s), xp.ph, abort)) break;
-          if (!mbar_wait(bar(B_WFULL + wp.s), wp.ph, abort)) break;
-          tc_fence_after();
-          const uint32_t a = w0 + wp.s * NP * kPlane, b = x0 + xp.s * kXBytes;
+        Place<kStages> sp(g0);
+        uint32_t j = (uint32_t)g0 * kTurns;  // turns before this one
+        bool go = true;
+        for (int kb = 0; kb < KB && go; ++kb, sp.step()) {
+          if (!mbar_wait(bar(B_FULL + sp.s), sp.ph, abort)) break;
+          const uint64_t da = make_desc(w0 + sp.s * kWBytes), db = make_desc(x0 + sp.s * kXBytes);
 #pragma unroll
-          for (int kk = 0; kk < kK / 16; ++kk)
+          for (int v = 0; v < kTurns; ++v, ++j) {
+            const uint32_t part = j % kParts;
+            // (passes at once for the first kParts)
+            go = mbar_wait(bar(B_ACCE + (int)part), ((j / kParts) & 1u) ^ 1u, abort);
+            if (!go) break;
+            tc_fence_after();
 #pragma unroll
-            for (int p = NP - 1; p >= 0; --p)  // the small plane first
-              mma_bf16(tmem_base, make_desc(a + p * kPlane + kk * 32), make_desc(b + kk * 32),
-                       idesc, (kc > 0 || kk > 0 || p < NP - 1) ? 1u : 0u);
-          mma_commit(bar(B_XEMPTY + xp.s));
-          mma_commit(bar(B_WEMPTY + wp.s));
+            for (int i = 0; i < kBatch * GROUP / 16; ++i) {
+              const int kk = v * (kBatch * GROUP / 16) + i;  // 16 columns, 32 bytes of a row
+              const uint32_t at = (kk / 4) * (kWHalf >> 4) + (kk % 4) * 2;
+              static_assert(kWHalf == kXHalf, "one offset for both operands");
+              mma_bf16(tmem_base + (part * kBatch + i / (GROUP / 16)) * kRows, da + at, db + at,
+                       idesc, i % (GROUP / 16) > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(B_ACCF + (int)part));
+          }
+          if (!go) break;
+          mma_commit(bar(B_EMPTY + sp.s));
         }
-        // also after an abort: every MMA is done before TMEM is read or freed
-        mma_commit(bar(B_ACC));
       }
       __syncwarp();
-    } else if (warp <= kCopyWarps) {
-      // ---- rows of x: copy i of a stage (ct + 128 u): row i / 8, 16-byte chunk i % 8 --
-      const int ct = tid - 32;
-      constexpr int kLag = kXStages - 1;
+    } else if (warp == 1) {
+      // ---- packed units, as they lie ------------------------------------------------
+      if (lane == 0) {
+        const uint8_t* src = P.wp + ((long)e * P.tiles + tile) * P.KB * (long)P.unit_bytes;
+        Place<kUnitStages> up(g0), last(g0);
+        int issued = 0;
+        for (; issued < KB; ++issued, up.step()) {
+          if (!mbar_wait(bar(B_UEMPTY + up.s), up.ph ^ 1u, abort)) break;
+          const uint32_t full = bar(B_UFULL + up.s);
+          mbar_arrive_expect_tx(full, (uint32_t)(tiles_here * P.unit_bytes));
+          for (int u = 0; u < tiles_here; ++u)
+            eg::bulk_load(u0 + (uint32_t)((2 * up.s + u) * P.unit_bytes),
+                          src + ((long)u * P.KB + issued) * P.unit_bytes, (uint32_t)P.unit_bytes,
+                          full);
+        }
+        // after a give-up: every copy lands before the CTA exits
+        for (int i = 0; i < issued; ++i, last.step())
+          if (i >= issued - kUnitStages) mbar_wait(bar(B_UFULL + last.s), last.ph, abort, true);
+      }
+      __syncwarp();
+    } else if (warp < 2 + kCopyWarps) {
+      // ---- rows of x: copy i of half a stage (ct + 64 u): row i / 8, chunk i % 8 -----
+      const int ct = tid - 64;
+      constexpr int kLag = 2;  // halves of a stage on their way
       auto hand_over = [&](int st) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kLag - 1) : "memory");
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_XFULL + st));
+        if (lane == 0) mbar_arrive(bar(B_FULL + st));
       };
       bool go = true;
-      // this thread's copies of a stage: rows r0 + 16 u, 16-byte chunk c
+      // this thread's copies: rows r0 + 8 u, 16-byte chunk c
       const int r0 = ct >> 3, c = ct & 7, n_rows = (rows + 15) / 16 * 16;
       const uint32_t dst0 = (uint32_t)r0 * 128u + ((uint32_t)(c ^ (r0 & 7)) << 4);
-      constexpr int kCopies = kRows / 16;  // 16 rows of 8 chunks per round
-      static_assert(32 * kCopyWarps == 16 * 8, "a round copies 16 rows");
+      constexpr int kCopies = kRows / 8;  // 8 rows of 8 chunks per round
+      static_assert(32 * kCopyWarps == 8 * 8, "a round copies 8 rows");
       const uint16_t* from[kCopies];
 #pragma unroll
-      for (int u = 0; u < kCopies; ++u) from[u] = P.x + (long)tok_s[r0 + 16 * u] * P.d + c * 8;
-      Place<kXStages> xp(g0), lag(g0);
-      for (int kc = 0; kc < KC; ++kc, xp.step()) {
+      for (int u = 0; u < kCopies; ++u) from[u] = P.x + (long)tok_s[r0 + 8 * u] * P.d + c * 8;
+      Place<kStages> xp(g0), lag(g0);
+      for (int kc = 0; kc < 2 * KB; ++kc) {
         if (kc >= kLag) {
           hand_over(lag.s);
-          lag.step();
+          if (kc & 1) lag.step();
         }
-        if (g0 + kc >= kXStages) {
-          go = __all_sync(0xffffffffu, mbar_wait(bar(B_XEMPTY + xp.s), xp.ph ^ 1u, abort));
+        if (!(kc & 1)) {
+          if (kc > 0) xp.step();
+          go = __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + xp.s), xp.ph ^ 1u, abort));
           if (!go) break;
         }
-        const uint32_t base = x0 + xp.s * kXBytes + dst0;
+        const uint32_t base = x0 + xp.s * kXBytes + (kc & 1) * kXHalf + dst0;
         const int col = kc * kK + c * 8;
         // columns past d: zeros (nothing is read)
         const uint32_t bytes = col < P.d ? 16u : 0u;
         const int at = col < P.d ? kc * kK : 0;
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
-          if (16 * u >= n_rows) break;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + u * 2048),
+          if (8 * u >= n_rows) break;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + u * 1024),
                        "l"(from[u] + at), "r"(bytes)
                        : "memory");
         }
@@ -314,119 +337,141 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_proxy_async();
       __syncwarp();
-      if (go && lane == 0)
-        for (int kc = KC - kLag < 0 ? 0 : KC - kLag; kc < KC; ++kc, lag.step())
-          mbar_arrive(bar(B_XFULL + lag.s));
-      // ---- TMEM lane = output row, column = row of x ------------------------------
-      const int q = warp & 3;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(B_ACC), (uint32_t)done & 1u, abort, true)) &&
-                      !*abort;
-      tc_fence_after();
-      const int col = out0 + q * 32 + lane;
-      for (int c0 = 0; c0 < rows; c0 += 16) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0, v);  // whole warp
-        if (ok && col < P.n_out) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c0 + i >= rows) break;
-            const __nv_bfloat16 b = __float2bfloat16_rn(v[i]);
-            P.out[(long)(row0 + c0 + i) * P.n_out + col] =
-                *reinterpret_cast<const uint16_t*>(&b);
-          }
-        }
+      static_assert(kLag == 2, "the last stage's halves are left");
+      if (go && lane == 0) {
+        mbar_arrive(bar(B_FULL + lag.s));
+        mbar_arrive(bar(B_FULL + lag.s));
       }
-    } else {
-      // ---- weights: unit u2 of the two, half h, m = 2 mh and 2 mh + 1, both steps --
-      const int wd = (warp - 1 - kCopyWarps) % kWidenWarps;
-      const int set = (warp - 1 - kCopyWarps) / kWidenWarps;
-      const int u2 = wd >> 2, h = (wd >> 1) & 1, mh = wd & 1;
-      const int tile = out0 / w4::kTile + u2;
-      const bool here = tile < P.tiles;
-      const uint8_t* src =
-          P.wp + ((long)e * P.tiles + (here ? tile : 0)) * P.KB * (long)P.unit_bytes;
-      // the words and the scales (m, then h; as loaded) of the next kAhead stages;
-      // each buffer is loaded again as soon as it has been read (moving them up
-      // would wait for the newest)
-      using Sc = typename std::conditional<sizeof(S) == 2, uint2, uint4>::type;
-      constexpr int kAhead = 3;
-      uint2 w[kAhead][2];
-      Sc sc[kAhead][2];
-      auto fetch = [&](int kc, int b) {
-        if (!here || kc >= KC) return;
-        const uint8_t* unit = src + (long)(kc >> 1) * P.unit_bytes;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int i = (kc & 1) * 2 + j;
-          w[b][j] =
-              __ldg(reinterpret_cast<const uint2*>(unit + 1024 * i + 512 * h + 16 * lane) + mh);
-          sc[b][j] = __ldg(reinterpret_cast<const Sc*>(unit + w4::kWeightBytes) +
-                           ((i * 32 / GROUP) * 8 + lane / 4) * 2 + mh);
-        }
-      };
+    } else if (warp < 2 + kCopyWarps + kWidenWarps) {
+      // ---- weights: unit u2 of the two, half h, every m and step ---------------------
+      const int wd = warp - 2 - kCopyWarps;
+      const int u2 = wd >> 1, h = wd & 1;
+      const bool here = u2 < tiles_here;
       // Rows of even and odd l / 4 store the two steps in opposite order, so that a
       // quarter warp's 16-byte stores (two rows) fall on distinct banks.
-      const bool odd = (lane / 4) & 1;
-      const uint32_t row = (uint32_t)(u2 * 64 + mh * 32 + 8 * h + lane / 4);
-#pragma unroll
-      for (int b = 0; b < kAhead; ++b) fetch(set + b * kWidenSets, b);
-      Place<kWStages> wp(g0 + set);
-      auto widen = [&](int kc, int b) {  // false: a wait gave up
-        uint2 wc[2];
-        Sc scc[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          wc[j] = odd ? w[b][1 - j] : w[b][j];
-          scc[j] = odd ? sc[b][1 - j] : sc[b][j];
-        }
-        fetch(kc + kAhead * kWidenSets, b);
-        if (g0 + kc >= kWStages &&
-            !__all_sync(0xffffffffu, mbar_wait(bar(B_WEMPTY + wp.s), wp.ph ^ 1u, abort)))
-          return false;
+      const int odd = (lane / 4) & 1;
+      const uint32_t row = (uint32_t)(u2 * 64 + 8 * h + lane / 4);
+      Place<kStages> wp(g0);
+      Place<kUnitStages> up(g0);
+      bool go;
+      for (int kb = 0; kb < KB; ++kb, wp.step(), up.step()) {
+        go = __all_sync(0xffffffffu, mbar_wait(bar(B_UFULL + up.s), up.ph, abort)) &&
+             __all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + wp.s), wp.ph ^ 1u, abort));
+        if (!go) break;
         if (here) {
-          uint8_t* a = smem + kXStages * kXBytes + wp.s * NP * kPlane + row * 128;
+          const uint8_t* unit =
+              smem + kUAt + (uint32_t)((2 * up.s + u2) * P.unit_bytes) + 512 * h + 16 * lane;
+          uint8_t* a = smem + kWAt + wp.s * kWBytes + row * 128;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t c = (uint32_t)((j ^ (int)odd) * 4 + lane % 4);
+          for (int i = 0; i < 4; ++i) {  // half i / 2 of the stage
+            const int step = i ^ odd;
+            const uint4 w = *reinterpret_cast<const uint4*>(unit + 1024 * step);
+            const uint32_t c = (uint32_t)((step & 1) * 4 + lane % 4) ^ (row & 7);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {  // output rows row + 16 m, r % 8 the same
-              S sv;
-              if constexpr (sizeof(S) == 2)
-                sv = (uint16_t)(h ? (m ? scc[j].y : scc[j].x) >> 16
-                                  : (m ? scc[j].y : scc[j].x) & 0xffffu);
-              else
-                sv = __uint_as_float(h ? (m ? scc[j].w : scc[j].y) : (m ? scc[j].z : scc[j].x));
-              uint32_t o[4][NP];
-#pragma unroll
-              for (int p = 0; p < 4; ++p)
-                planes2(weight2(m ? wc[j].y : wc[j].x, p), sv, o[p]);
-#pragma unroll
-              for (int pl = 0; pl < NP; ++pl)
-                *reinterpret_cast<uint4*>(a + pl * kPlane + m * 2048 + ((c ^ (row & 7)) << 4)) =
-                    make_uint4(o[0][pl], o[1][pl], o[2][pl], o[3][pl]);
-            }
+            for (int m = 0; m < 4; ++m)  // output rows row + 16 m, r % 8 the same
+              *reinterpret_cast<uint4*>(a + (i / 2) * kWHalf + m * 2048 + (c << 4)) =
+                  make_uint4(weight2(words[m], 0), weight2(words[m], 1), weight2(words[m], 2),
+                             weight2(words[m], 3));
           }
           fence_proxy_async();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_WFULL + wp.s));
-        wp.step(kWidenSets);
-        return true;
-      };
-      bool go = true;
-      for (int kc = set; kc < KC && go; kc += kAhead * kWidenSets) {
-#pragma unroll
-        for (int b = 0; b < kAhead; ++b)
-          if (go && kc + b * kWidenSets < KC) go = widen(kc + b * kWidenSets, b);
+        if (lane == 0) {
+          mbar_arrive(bar(B_FULL + wp.s));
+          mbar_arrive(bar(B_UEMPTY + up.s));
+        }
       }
+    } else {
+      // ---- sums: TMEM lane = output row, column = row of x; this warp's columns are
+      // 16 at a time, chunk wj + kStep i of them -----------------------------------------
+      constexpr int kStep = kSumWarps / 4, kChunks = kRows / 16 / kStep;
+      const int q = warp & 3, wj = (warp - 2 - kCopyWarps - kWidenWarps) >> 2;
+      const int n16 = (rows + 15) / 16;
+      const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+      const bool here = (q >> 1) < tiles_here;
+      const int ru = (q & 1) * 32 + lane;  // row of the unit
+      const uint8_t* scales = smem + kUAt + (uint32_t)((q >> 1) * P.unit_bytes) +
+                              w4::kWeightBytes +
+                              ((ru & 7) * 8 + (ru >> 4) * 2 + ((ru >> 3) & 1)) * (int)sizeof(S);
+      float acc[kChunks][16];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) acc[i][c] = 0.0f;
+      uint32_t j = (uint32_t)g0 * kTurns;
+      // the scales of the next unit: its place in the ring is free early
+      Place<kUnitStages> up(g0);
+      S next[kUnitGroups];
+      bool go;
+      auto fetch = [&]() {
+        go = __all_sync(0xffffffffu, mbar_wait(bar(B_UFULL + up.s), up.ph, abort));
+#pragma unroll
+        for (int i = 0; i < kUnitGroups; ++i)
+          next[i] = here && go ? *reinterpret_cast<const S*>(scales + 2 * up.s * P.unit_bytes +
+                                                             64 * i * sizeof(S))
+                               : S{};
+        __syncwarp();
+        if (go && lane == 0) mbar_arrive(bar(B_UEMPTY + up.s));
+        up.step();
+        return go;
+      };
+      fetch();
+      for (int kb = 0; kb < KB && go; ++kb) {
+        float s[kUnitGroups];
+#pragma unroll
+        for (int i = 0; i < kUnitGroups; ++i) s[i] = to_f32(next[i]);
+        if (kb + 1 < KB && !fetch()) break;
+#pragma unroll
+        for (int v = 0; v < kTurns; ++v, ++j) {
+          const uint32_t part = j % kParts;
+          go = __all_sync(0xffffffffu,
+                          mbar_wait(bar(B_ACCF + (int)part), (j / kParts) & 1u, abort));
+          if (!go) break;
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              if (wj + kStep * i >= n16) break;
+              float t[16];
+              tmem_ld16(tmem_base + lane_off + (part * kBatch + b) * kRows + (wj + kStep * i) * 16,
+                        t);
+#pragma unroll
+              for (int c = 0; c < 16; c += 2)
+                fma2(acc[i][c], acc[i][c + 1], s[v * kBatch + b], t[c], t[c + 1]);
+            }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_ACCE + (int)part));
+        }
+        if (!go) break;
+      }
+      const int col = out0 + q * 32 + lane;
+      if (go && col < P.n_out) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int r = (wj + kStep * i) * 16 + c;
+            if (r >= rows) break;
+            const __nv_bfloat16 b = __float2bfloat16_rn(acc[i][c]);
+            P.out[(long)(row0 + r) * P.n_out + col] = *reinterpret_cast<const uint16_t*>(&b);
+          }
+      }
+      __syncwarp();
     }
     tc_fence_before();
-    __syncthreads();  // the accumulator has been read, every stage consumed
+    __syncthreads();  // the sums are done, every stage consumed
     tc_fence_after();
     if (*abort) break;
   }
   if (warp == 0) {
+    if (lane == 0) {  // after a give-up: every MMA issued is done before TMEM is released
+      mma_commit(bar(B_DRAIN));
+      mbar_wait(bar(B_DRAIN), 0, abort, true);
+    }
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                  "r"(kTmem)
                  : "memory");

@@ -1861,7 +1861,7 @@ int launch_expert_w4(const mr::w4::Params& P, unsigned grid, int sms, cudaStream
     Q.unit_bytes = P.unit_bytes;
     Q.sms = P.sms;
     auto tile = mr::w4t::expert_w4_tile_kernel<GROUP, S>;
-    constexpr int tile_smem = (int)mr::w4t::smem_bytes(sizeof(S) == 2 ? 2 : 3);
+    const int tile_smem = (int)mr::w4t::smem_bytes(P.unit_bytes);
     if (cudaFuncSetAttribute(tile, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem) !=
         cudaSuccess)
       return MR_ERR_CUDA;
@@ -1936,7 +1936,7 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   // where not even all rows make one
   const long long_passes =
       n > mr::w4::kLongRows ? n / 16 + n / (mr::w4::kLongRows + 1) : 0;
-  P.tile_rows = long_passes * l.tiles > 1000 ? mr::w4::kLongRows : 0;
+  P.tile_rows = long_passes * l.tiles > mr::w4::kTilePasses ? mr::w4::kLongRows : 0;
   P.sms = sms;
   const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
   // two CTAs per SM where their rings fit (all but fp32 scales of 32 columns, or

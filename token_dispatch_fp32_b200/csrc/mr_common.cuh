@@ -32,6 +32,17 @@ __device__ __forceinline__ float mr_sigmoid(float L) {
   return __fdividef(1.0f, 1.0f + __expf(-L));
 }
 
+// c + a * b of two independent fp32 pairs in one instruction (each rounded as a
+// scalar fused multiply-add).
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a, float b0, float b1) {
+  uint64_t c, aa, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(aa), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(c));
+}
+
 // Total order used by every top-k: larger value first, lower index on ties.
 __device__ __forceinline__ bool mr_better(float va, int ia, float vb, int ib) {
   return va > vb || (va == vb && ia < ib);

@@ -47,17 +47,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// c + a * b of two independent fp32 pairs in one instruction (each rounded as a
-// scalar fused multiply-add).
-__device__ __forceinline__ void fma2(float& c0, float& c1, float a, float b0, float b1) {
-  uint64_t c, aa, b;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(aa), "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(c));
-}
-
 // One warp per token.  Sigmoid: slot[t*k + j] = dl_j (0 for an id outside
 // [0, N_r)); `dense` (optional) gets the whole row dL[t].  Softmax: slot is not
 // written; `dense` gets the row and `planes` its three bf16 planes [3][T][Np]
