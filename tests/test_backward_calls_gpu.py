@@ -35,3 +35,21 @@ def test_gate_gradients_in_a_row_on_one_workspace(T, d, want_dx):
     for i, (dx, dW) in enumerate(got):
         assert torch.equal(dW, ref[i % 2][1])
         assert dx is None or torch.equal(dx, ref[i % 2][0])
+
+
+@pytest.mark.parametrize("d", [64, 67])
+def test_an_id_named_by_four_slots_of_a_softmax_gate(d):
+    """Its slots' gradients add up in slot order, in whichever lane: 2^24 + 1 -
+    2^24 + 1 is 1 in fp32 (and 0, 1 or 2 in other orders).  Eight equal logits: p =
+    1/8, the mean (2^24 - 2^24) / 8 + (1 + 1) / 8, the entry 2.5 / 8 * (1 - 1/4)."""
+    T, N_r, k = 300, 8, 4
+    idx = _i32([[t % N_r] * k for t in range(T)])
+    dw = torch.tensor([2.0 ** 24, 1.0, -2.0 ** 24, 1.0], device="cuda").repeat(T, 1)
+    W = torch.eye(N_r, d, device="cuda")
+    dlog = torch.empty((T, N_r), device="cuda")
+    dx, _ = mr.mr_router_backward(torch.zeros((T, d), device="cuda"), W,
+                                  torch.zeros((T, N_r), device="cuda"), idx, dw, None, None, 2.5,
+                                  flags=mr.MR_SCORE_SOFTMAX, dlogits=dlog)
+    assert mr.mr_get_error() == mr.MR_OK
+    assert (dlog.gather(1, idx[:, :1].long()) == 0.234375).all()
+    assert torch.equal(dx[:, :N_r], dlog)

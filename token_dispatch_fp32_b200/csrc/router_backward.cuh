@@ -95,12 +95,13 @@ __global__ void __launch_bounds__(32 * kDlWarps)
     const float pj = ok ? expf(L[e] - mx) * inv : 0.0f;
     const float mean = warp_sum(gj * pj);
     // a chosen entry is scale * p * (sum of its slots' g - mean); its own sum
-    // first, then the difference, so no two large terms cancel late
-    float gs = gj;
+    // first, in slot order in each of an id's lanes, then the difference, so no
+    // two large terms cancel late
+    float gs = 0.0f;
     for (int j = 0; j < k; ++j) {
       const int ej = __shfl_sync(0xffffffffu, e, j);
       const float gg = __shfl_sync(0xffffffffu, gj, j);
-      if (ok && j != lane && ej == e) gs += gg;
+      if (ej == e) gs += gg;
     }
     const int Np = (N_r + 7) & ~7;
     auto put = [&](int i, float v) {
