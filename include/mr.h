@@ -679,9 +679,9 @@ int mr_gather_rows_backward(const void *dxs, int dtype,
  * dx) the inputs.  All products and sums have fp32-level accuracy and a fixed
  * order: fp32 fused multiply-adds, or for softmax's dense products the sums of
  * bf16 planes' products on the tensor cores (as the forward's bf16x3).  Entries
- * of perm out of range inside a segment, or offsets that overlap, raise the
- * device flag (MR_ERR_DEVICE).  Calls that may overlap need different
- * workspaces.
+ * of perm out of range inside a segment, and offsets that decrease or lie
+ * outside [0, T*k], raise the device flag (MR_ERR_DEVICE); dW is then not
+ * defined.  Calls that may overlap need different workspaces.
  * Limits: N_r <= 512, 1 <= k <= 32, at least one of dlogits, dx and dW; sizes
  * past a launch's grid (rows of 8 million elements that no vector fits, softmax
  * with 8 million tokens off the tensor cores) return MR_ERR_UNSUPPORTED.

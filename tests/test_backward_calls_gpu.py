@@ -53,3 +53,26 @@ def test_an_id_named_by_four_slots_of_a_softmax_gate(d):
     assert mr.mr_get_error() == mr.MR_OK
     assert (dlog.gather(1, idx[:, :1].long()) == 0.234375).all()
     assert torch.equal(dx[:, :N_r], dlog)
+
+
+@pytest.mark.parametrize("T", [60, 900])
+@pytest.mark.parametrize("place", ["first", "inside", "last"])
+def test_offsets_that_overlap_or_leave_the_rows_are_flagged(T, place):
+    """One row too far is enough, in a batch whose segments make one piece each
+    too; the plan itself is not flagged."""
+    d, N_r, k = 64, 16, 2
+    _, x, W, L, idx, g = _gate_problem(T, d, N_r, k, "bf16", "f32", 0, seed=T)
+    _, offsets, perm, _ = oracle.dispatch(idx, N_r)
+    args = (_dev(x), _dev(W), _f32(L), _i32(idx), _f32(g), _i32(perm))
+    ref = mr.mr_router_backward(*args, _i32(offsets), 2.5)
+    assert mr.mr_get_error() == mr.MR_OK
+    bad = offsets.copy()
+    if place == "first":
+        bad[0] = -1
+    elif place == "inside":
+        bad[5] = bad[4] - 1  # the row before segment 4's is also segment 5's
+    else:
+        bad[N_r] += 1
+    dx, _ = mr.mr_router_backward(*args, _i32(bad), 2.5)
+    assert mr.mr_get_error() == mr.MR_ERR_DEVICE
+    assert torch.equal(dx, ref[0])

@@ -429,11 +429,8 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ offsets,
         found.row0 = lo + (i << sh);
         found.rows = cnt - (i << sh) < (1 << sh) ? cnt - (i << sh) : 1 << sh;
         found.extra = i == 0 ? -1 : xb + i - 1;
-        // more extra pieces than `part` holds: offsets that overlap
-        if (found.extra >= n >> sh) {
-          found.e = -1;
-          mr_raise(MR_FLAG_BAD_INDEX);
-        }
+        // more extra pieces than `part` holds: offsets that overlap (flagged)
+        if (found.extra >= n >> sh) found.e = -1;
         break;
       }
       before += p;
@@ -481,6 +478,10 @@ __global__ void __launch_bounds__(kDwThreads)
   // kernel starts; then only this kernel's end waits for that one's, so that
   // whatever follows on the stream comes after both.
   if (wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // one CTA: the segments lie in order, inside the rows
+    for (int e = threadIdx.x; e <= N_r; e += kDwThreads)
+      if (offsets[e] < 0 || offsets[e] > n || (e < N_r && offsets[e + 1] < offsets[e]))
+        mr_raise(MR_FLAG_BAD_INDEX);
   const Piece pc = find_piece(offsets, N_r, n, sh, blockIdx.x);
   if (pc.e < 0) {
     if (!wait_first) asm volatile("griddepcontrol.wait;" ::: "memory");
