@@ -44,7 +44,7 @@
 // hold the value 0 (nibble 8) and scale 0.
 //
 // The kernel is persistent, two CTAs per SM.  An item is 64 output rows of one
-// expert against up to `xr` of its sorted rows; a team of `ks` of the CTA's
+// expert against up to 16 of its sorted rows; a team of `ks` of the CTA's
 // eight warps (chosen from the number of items) takes it, splits its columns
 // (member m takes units m, m + ks, ..) and meets in shared memory at the item's
 // end, adding in member order.  Each warp has its own ring of units in shared
@@ -70,7 +70,6 @@ constexpr int kCols = 128;     // columns per unit
 constexpr int kWeightBytes = kTile * kCols / 2;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxExperts = 1024;
 constexpr int kStages = 2;     // units per warp's ring
 constexpr int kRowsPerPass = 16;  // sorted rows per item (two column tiles of the MMA)
 
@@ -156,7 +155,7 @@ struct Params {
   const int32_t* offsets;
   const uint8_t* wp;
   uint16_t* out;
-  int T, d, k, N_r, n_out, tiles, KB, unit_bytes, xr;
+  int T, d, k, N_r, n_out, tiles, KB, unit_bytes;
   int tile_rows;  // segments of more rows may go to expert_w4_tile.cuh's kernel (0: never)
   int sms;
 };
@@ -238,7 +237,7 @@ __device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const ui
 
 // Whether the segments of more than kLongRows rows go to the many-row kernel
 // (expert_w4_tile.cuh), decided alike by both kernels from the segments:
-// `passes` passes of 16 of their rows here, or `blocks` blocks there.  There a
+// `passes` passes of kRowsPerPass of their rows here, or `blocks` blocks there.  There a
 // 128-row tile of n_out takes an SM 1.0 to 1.4 us for 128 columns, however few the
 // rows of its block; here a unit and pass takes the whole GPU 1.4 to 2 ns.
 // Measured (d = 7168, n_out = 2048, groups of 32, bf16 scales), here / there: 4 x 64
@@ -247,6 +246,9 @@ __device__ __forceinline__ void step(const uint8_t* w, int i, int lane, const ui
 // 89, 256 x 128 rows 4.9 / 2.2 ms; groups of 128 with fp32 scales, 8 x 48 rows 87 / 71;
 // d = 1408, n_out = 512, 40 x 64 rows (640) 53 / 42.
 constexpr int kLongRows = 32;
+__device__ __forceinline__ int passes_of(int rows) {
+  return (rows + kRowsPerPass - 1) / kRowsPerPass;
+}
 constexpr int kTileRows = 128;     // rows per block there
 constexpr int kTilePasses = 700;   // units and passes that take as long as a wave there
 __device__ __forceinline__ bool long_to_tile(long passes, long blocks, int n_out, int sms) {
@@ -280,7 +282,7 @@ struct Shared {
   uint64_t bars[kWarps][kStages];
   int wsum[kWarps], pair[2 * kWarps];
   int abort;
-  int* first;  // [N_r + 1] passes of xr rows before expert e
+  int* first;  // [N_r + 1] passes before expert e
   int* off;    // [N_r + 1] the experts' segments
   float* red;  // [2][kRed]
 };
@@ -306,8 +308,8 @@ __device__ __forceinline__ void find(const Params& P, const Shared& sh, Walk& k)
     else hi = mid - 1;
   }
   k.e = lo;
-  k.row0 = sh.off[lo] + (pass - sh.first[lo]) * P.xr;
-  k.rows = min(sh.off[lo + 1] - k.row0, P.xr);
+  k.row0 = sh.off[lo] + (pass - sh.first[lo]) * kRowsPerPass;
+  k.rows = min(sh.off[lo + 1] - k.row0, kRowsPerPass);
 }
 
 template <int GROUP, typename S>
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
       for (int e = e0; e < e1; ++e) {
         const int rows = sh.off[e + 1] - sh.off[e];
         if (rows > P.tile_rows) {
-          lp += (rows + 15) / 16;
+          lp += passes_of(rows);
           lb += (rows + kTileRows - 1) / kTileRows;
         }
       }
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_w4_kernel(const Params P) 
     auto passes = [&](int e) {
       const int rows = sh.off[e + 1] - sh.off[e];
       if (rows <= 0 || (without_long && rows > P.tile_rows)) return 0;
-      return (rows + P.xr - 1) / P.xr;
+      return passes_of(rows);
     };
     int mine = 0;
     for (int e = e0; e < e1; ++e) mine += passes(e);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_tile_kernel(const Param
     int lp = 0;
     for (int e = e0; e < e1; ++e) {
       const int rows = segment(e, a);
-      lp += (rows + 15) / 16;
+      lp += w4::passes_of(rows);
       mine += (rows + kRows - 1) / kRows;
     }
     int lb = mine;

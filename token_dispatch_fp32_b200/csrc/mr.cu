@@ -1929,16 +1929,15 @@ int mr_expert_gemv_gather_w4(const void* x, const int32_t* perm, const int32_t* 
   P.unit_bytes = l.unit_bytes;
   int sms = 0, cc = 0;
   if (!device_info(&sms, &cc)) return MR_ERR_CUDA;
-  // rows of x per pass over an expert's weights
   const long n = (long)T * k;
-  P.xr = mr::w4::kRowsPerPass;
+  constexpr int kPass = mr::w4::kRowsPerPass;
   // the most passes that long segments can have (mr::w4::long_to_tile); none
   // where not even all rows make one
   const long long_passes =
-      n > mr::w4::kLongRows ? n / 16 + n / (mr::w4::kLongRows + 1) : 0;
+      n > mr::w4::kLongRows ? n / kPass + n / (mr::w4::kLongRows + 1) : 0;
   P.tile_rows = long_passes * l.tiles > mr::w4::kTilePasses ? mr::w4::kLongRows : 0;
   P.sms = sms;
-  const long items = (n / P.xr + std::min<long>(n, N_r)) * l.tiles;  // at most
+  const long items = (n / kPass + std::min<long>(n, N_r)) * l.tiles;  // at most
   // two CTAs per SM where their rings fit (all but fp32 scales of 32 columns, or
   // more than about 600 experts)
   const long per_sm = mr::w4::smem_bytes(l.unit_bytes, N_r) <= 113 * 1024 ? 2 : 1;
