@@ -150,14 +150,25 @@ def _call(fn: str, dev, stream, *args) -> None:
         raise MRError(fn, status)
 
 
-def _scratch(nbytes, dev, stream):
+def _scratch(shape, dtype, dev, stream):
     """A workspace for one call on `stream` (None: the current stream).  It is
     freed when the call returns, so it comes from that stream's own memory: the
     allocator hands it out again behind the call's kernels, never beside them."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _new(shape, dtype, dev, stream):
+    """An output that a call on `stream` allocates: from that stream's own memory
+    too (the current stream's may still be written by what that stream has to
+    do), and marked as used by the current stream, where the caller reads and
+    frees it."""
+    t = _scratch(shape, dtype, dev, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _device_of(*tensors):
@@ -208,9 +219,9 @@ def mr_router_forward(x, W, bias, n_group, topk_group, k, route_scale, mask_mode
     _need(W, "W", torch.float32, (N_r, d))
     if bias is not None:
         _need(bias, "bias", torch.float32, (N_r,))
-    idx_out = torch.empty((T, k), dtype=torch.int32, device=x.device) if idx_out is None else \
+    idx_out = _new((T, k), torch.int32, x.device, stream) if idx_out is None else \
         _need(idx_out, "idx_out", torch.int32, (T, k))
-    w_out = torch.empty((T, k), dtype=torch.float32, device=x.device) if w_out is None else \
+    w_out = _new((T, k), torch.float32, x.device, stream) if w_out is None else \
         _need(w_out, "w_out", torch.float32, (T, k))
     dev = _device_of(x, W, bias, idx_out, w_out)
     _call("mr_router_forward", dev, stream, _ptr(x), _ptr(W), _ptr(bias), T, d, N_r, n_group,
@@ -240,9 +251,9 @@ def mr_router_forward_ex(x, W, bias, n_group, topk_group, k, route_scale, mask_m
     _need(W, "W", torch.float32, (N_r, d))
     if bias is not None:
         _need(bias, "bias", torch.float32, (N_r,))
-    idx_out = torch.empty((T, k), dtype=torch.int32, device=x.device) if idx_out is None else \
+    idx_out = _new((T, k), torch.int32, x.device, stream) if idx_out is None else \
         _need(idx_out, "idx_out", torch.int32, (T, k))
-    w_out = torch.empty((T, k), dtype=torch.float32, device=x.device) if w_out is None else \
+    w_out = _new((T, k), torch.float32, x.device, stream) if w_out is None else \
         _need(w_out, "w_out", torch.float32, (T, k))
     if logits_out is not None:
         _need(logits_out, "logits_out", torch.float32, (T, N_r))
@@ -275,9 +286,9 @@ def mr_router_forward_bf16w(x, W_bf16, bias, n_group, topk_group, k, route_scale
     _need(W_bf16, "W_bf16", torch.bfloat16, (N_r, d))
     if bias is not None:
         _need(bias, "bias", torch.float32, (N_r,))
-    idx_out = torch.empty((T, k), dtype=torch.int32, device=x.device) if idx_out is None else \
+    idx_out = _new((T, k), torch.int32, x.device, stream) if idx_out is None else \
         _need(idx_out, "idx_out", torch.int32, (T, k))
-    w_out = torch.empty((T, k), dtype=torch.float32, device=x.device) if w_out is None else \
+    w_out = _new((T, k), torch.float32, x.device, stream) if w_out is None else \
         _need(w_out, "w_out", torch.float32, (T, k))
     if logits_out is not None:
         _need(logits_out, "logits_out", torch.float32, (T, N_r))
@@ -304,19 +315,19 @@ def mr_dispatch(idx, N_r, counts=None, offsets=None, perm=None, inv_perm=None, w
     _need(idx, "idx", torch.int32)
     T, k = idx.shape
     dev = idx.device
-    counts = torch.empty(N_r, dtype=torch.int32, device=dev) if counts is None else \
+    counts = _new(N_r, torch.int32, dev, stream) if counts is None else \
         _need(counts, "counts", torch.int32, (N_r,))
-    offsets = torch.empty(N_r + 1, dtype=torch.int32, device=dev) if offsets is None else \
+    offsets = _new(N_r + 1, torch.int32, dev, stream) if offsets is None else \
         _need(offsets, "offsets", torch.int32, (N_r + 1,))
-    perm = torch.empty(T * k, dtype=torch.int32, device=dev) if perm is None else \
+    perm = _new(T * k, torch.int32, dev, stream) if perm is None else \
         _need(perm, "perm", torch.int32, (T * k,))
     if inv_perm is None and want_inv:
-        inv_perm = torch.empty(T * k, dtype=torch.int32, device=dev)
+        inv_perm = _new(T * k, torch.int32, dev, stream)
     elif inv_perm is not None:
         _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     need = mr_dispatch_workspace_size(T, k, N_r)
     if workspace is None:
-        workspace = _scratch(max(need, 4), dev, stream)
+        workspace = _scratch(max(need, 4), torch.uint8, dev, stream)
     _need(workspace, "workspace")
     _call("mr_dispatch", _device_of(idx, counts, offsets, perm, inv_perm, workspace), stream,
           _ptr(idx), T, k, N_r, _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv_perm),
@@ -354,13 +365,13 @@ def mr_ep_recv_order(recv_counts, R, order=None, inv_order=None, local_counts=No
     _need(recv_counts, "recv_counts", torch.int32)
     ep, E_loc = recv_counts.shape
     dev = recv_counts.device
-    order = torch.empty(R, dtype=torch.int32, device=dev) if order is None else \
+    order = _new(R, torch.int32, dev, stream) if order is None else \
         _need(order, "order", torch.int32, (R,))
-    inv_order = torch.empty(R, dtype=torch.int32, device=dev) if inv_order is None else \
+    inv_order = _new(R, torch.int32, dev, stream) if inv_order is None else \
         _need(inv_order, "inv_order", torch.int32, (R,))
-    local_counts = torch.empty(E_loc, dtype=torch.int32, device=dev) if local_counts is None \
+    local_counts = _new(E_loc, torch.int32, dev, stream) if local_counts is None \
         else _need(local_counts, "local_counts", torch.int32, (E_loc,))
-    local_offsets = torch.empty(E_loc + 1, dtype=torch.int32, device=dev) \
+    local_offsets = _new(E_loc + 1, torch.int32, dev, stream) \
         if local_offsets is None else _need(local_offsets, "local_offsets", torch.int32,
                                             (E_loc + 1,))
     _call("mr_ep_recv_order", _device_of(recv_counts, order, inv_order, local_counts,
@@ -388,7 +399,7 @@ def mr_expert_gemm_gather(x, k, perm, offsets, W_exp, out=None, stream=None):
     if dw != d:
         raise ValueError(f"W_exp is [N_r, n_out, {dw}], x rows have {d} columns")
     _need(offsets, "offsets", torch.int32, (N_r + 1,))
-    out = torch.empty((T * k, n_out), dtype=torch.bfloat16, device=x.device) if out is None \
+    out = _new((T * k, n_out), torch.bfloat16, x.device, stream) if out is None \
         else _need(out, "out", torch.bfloat16, (T * k, n_out))
     _call("mr_expert_gemm_gather", _device_of(x, perm, offsets, W_exp, out), stream,
           _ptr(x), _ptr(perm), _ptr(offsets), _ptr(W_exp), T, d, k, N_r, n_out, _ptr(out))
@@ -401,7 +412,7 @@ def mr_expert_pack_weights(W_exp, stream=None):
     _need(W_exp, "W_exp", torch.bfloat16)
     N_r, n_out, d = W_exp.shape
     n = int(lib().mr_expert_packed_bytes(N_r, n_out, d))
-    Wp = torch.empty(n // 2, dtype=torch.bfloat16, device=W_exp.device)
+    Wp = _new(n // 2, torch.bfloat16, W_exp.device, stream)
     _call("mr_expert_pack_weights", _device_of(W_exp, Wp), stream, _ptr(W_exp), N_r, n_out, d,
           _ptr(Wp), n)
     return Wp
@@ -422,7 +433,7 @@ def mr_expert_gemm_gather_packed(x, k, perm, offsets, W_packed, N_r, n_out, out=
     _need(W_packed, "W_packed", torch.bfloat16)
     if W_packed.numel() * 2 < int(lib().mr_expert_packed_bytes(N_r, n_out, d)):
         raise ValueError("W_packed is smaller than mr_expert_packed_bytes")
-    out = torch.empty((T * k, n_out), dtype=torch.bfloat16, device=x.device) if out is None \
+    out = _new((T * k, n_out), torch.bfloat16, x.device, stream) if out is None \
         else _need(out, "out", torch.bfloat16, (T * k, n_out))
     _call("mr_expert_gemm_gather_packed", _device_of(x, perm, offsets, W_packed, out), stream,
           _ptr(x), _ptr(perm), _ptr(offsets), _ptr(W_packed), T, d, k, N_r, n_out, _ptr(out))
@@ -455,9 +466,9 @@ def mr_expert_gemm_gather_combine(x, k, perm, offsets, W, w, shared=None, N_r=No
     _need(w, "w", torch.float32, (T, k))
     if shared is not None:
         _need(shared, "shared", torch.bfloat16, (T, n_out))
-    acc = torch.empty((T, n_out), dtype=torch.float32, device=x.device) if acc is None \
+    acc = _scratch((T, n_out), torch.float32, x.device, stream) if acc is None \
         else _need(acc, "acc", torch.float32, (T, n_out))
-    y = torch.empty((T, n_out), dtype=torch.bfloat16, device=x.device) if y is None \
+    y = _new((T, n_out), torch.bfloat16, x.device, stream) if y is None \
         else _need(y, "y", torch.bfloat16, (T, n_out))
     _call("mr_expert_gemm_gather_combine", _device_of(x, perm, offsets, W, w, shared, acc, y),
           stream, _ptr(x), _ptr(perm), _ptr(offsets), _ptr(W), 1 if packed else 0, _ptr(w),
@@ -474,7 +485,7 @@ def mr_gather_rows(x, k, perm=None, inv_perm=None, xs=None, stream=None):
         _need(perm, "perm", torch.int32, (T * k,))
     if inv_perm is not None:
         _need(inv_perm, "inv_perm", torch.int32, (T * k,))
-    xs = torch.empty((T * k, d), dtype=x.dtype, device=x.device) if xs is None else \
+    xs = _new((T * k, d), x.dtype, x.device, stream) if xs is None else \
         _need(xs, "xs", x.dtype, (T * k, d))
     _call("mr_gather_rows", _device_of(x, perm, inv_perm, xs), stream, _ptr(x), dt, T, d, k,
           _ptr(perm), _ptr(inv_perm), _ptr(xs))
@@ -492,7 +503,7 @@ def mr_combine(expert_out, w, inv_perm, shared=None, y=None, stream=None):
     _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     if shared is not None:
         _need(shared, "shared", expert_out.dtype, (T, d))
-    y = torch.empty((T, d), dtype=expert_out.dtype, device=expert_out.device) if y is None else \
+    y = _new((T, d), expert_out.dtype, expert_out.device, stream) if y is None else \
         _need(y, "y", expert_out.dtype, (T, d))
     _call("mr_combine", _device_of(expert_out, w, inv_perm, shared, y), stream,
           _ptr(expert_out), dt, _ptr(w), _ptr(inv_perm), _ptr(shared), _ptr(y), T, d, k)
@@ -517,11 +528,11 @@ def mr_combine_backward(dy, expert_out, w, inv_perm, dexpert=None, dw=None, want
     if dexpert is not None:
         _need(dexpert, "dexpert", dy.dtype, (T * k, d))
     elif want_dexpert:
-        dexpert = dy.new_empty((T * k, d))
+        dexpert = _new((T * k, d), dy.dtype, dy.device, stream)
     if dw is not None:
         _need(dw, "dw", torch.float32, (T, k))
     elif want_dw:
-        dw = torch.empty_like(w)
+        dw = _new((T, k), torch.float32, w.device, stream)
     if dw is not None and expert_out is None:
         raise ValueError("dw needs expert_out")
     _call("mr_combine_backward", _device_of(dy, expert_out, w, inv_perm, dexpert, dw), stream,
@@ -542,7 +553,7 @@ def mr_gather_rows_backward(dxs, k, inv_perm, add=None, dx=None, stream=None):
     _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     if add is not None:
         _need(add, "add", dxs.dtype, (T, d))
-    dx = dxs.new_empty((T, d)) if dx is None else \
+    dx = _new((T, d), dxs.dtype, dxs.device, stream) if dx is None else \
         _need(dx, "dx", dxs.dtype, (T, d))
     _call("mr_gather_rows_backward", _device_of(dxs, inv_perm, add, dx), stream, _ptr(dxs), dt,
           _ptr(inv_perm), _ptr(add), T, d, k, _ptr(dx))
@@ -586,14 +597,14 @@ def mr_router_backward(x, W, logits, idx, dw, perm, offsets, route_scale, flags=
     if dx is not None:
         _need(dx, "dx", x.dtype, (T, d))
     elif want_dx:
-        dx = torch.empty_like(x)
+        dx = _new((T, d), x.dtype, x.device, stream)
     if dW is not None:
         _need(dW, "dW", torch.float32, (N_r, d))
     elif want_dW:
-        dW = torch.empty((N_r, d), dtype=torch.float32, device=x.device)
+        dW = _new((N_r, d), torch.float32, x.device, stream)
     if workspace is None:
         workspace = _scratch(max(mr_router_backward_workspace_size(T, d, N_r, k, flags), 16),
-                             x.device, stream)
+                             torch.uint8, x.device, stream)
     _need(workspace, "workspace")
     _call("mr_router_backward", _device_of(x, W, logits, idx, dw, perm, offsets, add, dlogits, dx,
                                            dW, workspace), stream,
@@ -617,7 +628,7 @@ def mr_expert_pack_w4(q, scales, group, stream=None):
     if n == 0:
         raise MRError("mr_expert_pack_w4", MR_ERR_UNSUPPORTED)
     _need(scales, "scales", None, (N_r, n_out, -(-d // group)))
-    packed = torch.empty(n, dtype=torch.uint8, device=q.device)
+    packed = _new(n, torch.uint8, q.device, stream)
     _call("mr_expert_pack_w4", _device_of(q, scales, packed), stream, _ptr(q), _ptr(scales), sdt,
           N_r, n_out, d, group, _ptr(packed), n)
     return packed
@@ -647,7 +658,7 @@ def mr_expert_gemv_gather_w4(x, k, perm, offsets, packed, N_r, n_out, group,
         raise MRError("mr_expert_gemv_gather_w4", MR_ERR_UNSUPPORTED)
     if packed.numel() != n:
         raise ValueError(f"packed has {packed.numel()} bytes, these sizes need {n}")
-    out = torch.empty((T * k, n_out), dtype=torch.bfloat16, device=x.device) if out is None \
+    out = _new((T * k, n_out), torch.bfloat16, x.device, stream) if out is None \
         else _need(out, "out", torch.bfloat16, (T * k, n_out))
     _call("mr_expert_gemv_gather_w4", _device_of(x, perm, offsets, packed, out), stream, _ptr(x),
           _ptr(perm), _ptr(offsets), _ptr(packed), sdt, T, d, k, N_r, n_out, group, _ptr(out))
@@ -692,11 +703,11 @@ def mr_ep_dispatch_p2p(x, idx, inv_perm, offsets, counts_all, rank, recv_bufs, c
         raise ValueError(f"{N_r} experts do not split over {ep} ranks")
     E_loc = N_r // ep
     dev = _device_of(x, idx, inv_perm, offsets, counts_all)
-    dest = torch.empty(T * k, dtype=torch.int32, device=dev) if dest is None else \
+    dest = _new(T * k, torch.int32, dev, stream) if dest is None else \
         _need(dest, "dest", torch.int32, (T * k,))
-    local_counts = torch.empty(E_loc, dtype=torch.int32, device=dev) if local_counts is None \
+    local_counts = _new(E_loc, torch.int32, dev, stream) if local_counts is None \
         else _need(local_counts, "local_counts", torch.int32, (E_loc,))
-    local_offsets = torch.empty(E_loc + 1, dtype=torch.int32, device=dev) \
+    local_offsets = _new(E_loc + 1, torch.int32, dev, stream) \
         if local_offsets is None else _need(local_offsets, "local_offsets", torch.int32,
                                             (E_loc + 1,))
     _call("mr_ep_dispatch_p2p", _device_of(x, dest, local_counts, local_offsets), stream,
@@ -722,7 +733,7 @@ def mr_ep_combine_p2p(out_bufs, w, idx, dest, N_r, capacity, d, dtype, shared=No
         raise TypeError("rows must be bfloat16 or float32")
     if shared is not None:
         _need(shared, "shared", dtype, (T, d))
-    y = torch.empty((T, d), dtype=dtype, device=dev) if y is None else \
+    y = _new((T, d), dtype, dev, stream) if y is None else \
         _need(y, "y", dtype, (T, d))
     ep = len(out_bufs)
     _call("mr_ep_combine_p2p", _device_of(w, idx, dest, shared, y), stream,
