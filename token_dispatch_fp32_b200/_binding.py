@@ -131,6 +131,16 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream_of():
+    """device index -> handle of its current stream: torch's short way to it (7 us
+    less per call), the public one in a torch that has no such function."""
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_raw_stream = _raw_stream_of()
+
+
 def _call(fn: str, dev, stream, *args) -> None:
     """Calls C entry point `fn` with `dev` as the current CUDA device and the
     stream handle as the last argument: the library launches on the current
@@ -140,7 +150,7 @@ def _call(fn: str, dev, stream, *args) -> None:
         with torch.cuda.device(dev):
             return _call(fn, dev, stream, *args)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        handle = _raw_stream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
     else:
