@@ -635,8 +635,10 @@ int mr_combine_backward(const void *dy, int dtype, const void *expert_out,
  *   add       [T, d] of `dtype` added to the sum (the gradient of x's other
  *             uses, e.g. the shared expert), or NULL.  May be dx itself.
  *   dx        [T, d] of `dtype`: dx[t] = sum_j dxs[inv_perm[t*k+j]] + add[t],
- *             summed in fp32 in slot order, rounded once.  Must not overlap
- *             dxs.
+ *             summed in fp32 in a fixed order, rounded once: slot order, but for
+ *             bf16 rows that no 16-byte vector fits (d no multiple of 8, or a
+ *             buffer's start) first the rows that start on a 4-byte word, then
+ *             the others.  Must not overlap dxs.
  * One kernel, no atomics.  Limits: 1 <= k <= 32.
  */
 int mr_gather_rows_backward(const void *dxs, int dtype,
@@ -706,21 +708,33 @@ int mr_router_backward(const void *x, int x_dtype, const void *W, int W_dtype,
  *   q         [N_r, n_out, d/2] bytes: column 2i in the low nibble of byte i,
  *             column 2i+1 in the high one; nibble u stands for u - 8.
  *   scales    [N_r, n_out, ceil(d / group)] of scale_dtype (MR_BF16 or MR_F32).
- *   packed    the layout the kernel streams (16 x 128 blocks in the order the
- *             tensor core's lanes read them, then the scales in their own
- *             type), mr_expert_w4_packed_bytes bytes, caller-owned, 16-byte
+ *   packed    the layout the kernels stream (64 x 128 blocks in the order the
+ *             tensor core's lanes read them, each with its scales in their
+ *             own type), mr_expert_w4_packed_bytes bytes, caller-owned, 16-byte
  *             aligned; written once, when the weights are loaded.
  *   x, perm, offsets, out   as mr_expert_gemm_gather (perm NULL: x holds the
  *             sorted rows); rows of out from offsets[N_r] on are not written.
- * x times the 4-bit integers is exact in fp32; each group's fp32 sum is scaled
- * and added in fp32, and the result rounded to bf16 once.  One kernel, no
- * workspace, a fixed order of sums.  Any number of tokens is right; an expert's
- * weights are read again for every 16 of its rows, so larger batches are
- * better served by mr_expert_gemm_gather.
+ * x times the 4-bit integers is exact in fp32; each group's sum is formed in
+ * fp32, scaled and added in fp32, and the result rounded to bf16 once.  No
+ * workspace, no atomics.  Two kernels share the work, one or two launches:
+ *   - segments of up to 32 rows take passes of 16 rows over the expert's weights.
+ *     The sums of 32 columns run through at most 55 sum |x| (the weights enter as
+ *     16 + u, the offset separately) and are off by at most 440 * 2^-23 sum |x|;
+ *   - longer segments may take passes of up to 128 rows on the tensor cores'
+ *     fp32 accumulators, one accumulation per group (each 16 columns off by at
+ *     most 2 * 2^-23 of the group's sum of magnitudes), where the passes and rows
+ *     of all segments together make that faster.
+ * The same call gives the same bits; a row's last bits may depend on the other
+ * segments of its batch.  Any number of tokens is right; larger batches are better
+ * served by mr_expert_gemm_gather where memory holds bf16 weights.
+ * x is meant to be finite: a row with an infinity or a NaN has no finite output
+ * (an infinity may come out as NaN where the formula has an infinity), other
+ * rows are not touched by it.
  * mr_expert_w4_packed_bytes returns 0 for arguments it does not know.
- * Limits: group 32, 64 or 128, d % 8 == 0, N_r <= 1024, N_r * n_out < 2^31,
- * T*k <= 2^24, 16-byte aligned x (else MR_ERR_UNSUPPORTED).  An entry of perm
- * outside [0, T*k) inside a segment raises the device flag (MR_ERR_DEVICE).
+ * Limits: group 32, 64 or 128, d % 8 == 0, N_r <= 1024, T*k <= 2^24, 16-byte
+ * aligned x and packed (else MR_ERR_UNSUPPORTED); N_r * n_out < 2^31 (else
+ * MR_ERR_INVALID_ARG).  An entry of perm outside [0, T*k) inside a segment raises
+ * the device flag (MR_ERR_DEVICE).
  */
 size_t mr_expert_w4_packed_bytes(int N_r, int n_out, int d, int group,
                                  int scale_dtype);

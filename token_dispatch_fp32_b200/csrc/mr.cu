@@ -1480,13 +1480,16 @@ RouterBwdWs router_bwd_ws(int T, int d, int N_r, int k, int flags) {
     w.planes = take((size_t)3 * T * ((N_r + 7) & ~7) * 2);
     w.w_planes = take((size_t)3 * N_r * d * 2);
     // as many slices of at least 512 tokens as leave the fewest SMs idle in the
-    // last wave of 128 x 256 tiles (148 SMs), at most 8
+    // last wave of 128 x 256 tiles, at most 8.  The B200's 148 SMs, whatever the
+    // device: the size depends on the arguments alone, so that it can be asked for
+    // before a device is chosen.
+    constexpr long kSms = 148;
     const long tiles = (long)((N_r + mr::tc::BM - 1) / mr::tc::BM) *
                        ((d + mr::pg::kBN - 1) / mr::pg::kBN);
     double best = 0;
     for (int z = 1; z <= 8 && (z == 1 || T / z >= 512); ++z) {
-      const long waves = (tiles * z + 147) / 148;
-      const double eff = (double)(tiles * z) / (waves * 148);
+      const long waves = (tiles * z + kSms - 1) / kSms;
+      const double eff = (double)(tiles * z) / (waves * kSms);
       if (z == 1 || eff > best + 0.02) {
         best = eff;
         w.slices = z;
