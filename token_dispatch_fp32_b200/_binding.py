@@ -538,11 +538,13 @@ def mr_combine_backward(dy, expert_out, w, inv_perm, dexpert=None, dw=None, want
     if dexpert is not None:
         _need(dexpert, "dexpert", dy.dtype, (T * k, d))
     elif want_dexpert:
-        dexpert = _new((T * k, d), dy.dtype, dy.device, stream)
+        dexpert = dy.new_empty((T * k, d)) if stream is None else \
+            _new((T * k, d), dy.dtype, dy.device, stream)
     if dw is not None:
         _need(dw, "dw", torch.float32, (T, k))
     elif want_dw:
-        dw = _new((T, k), torch.float32, w.device, stream)
+        dw = torch.empty_like(w) if stream is None else \
+            _new((T, k), torch.float32, w.device, stream)
     if dw is not None and expert_out is None:
         raise ValueError("dw needs expert_out")
     _call("mr_combine_backward", _device_of(dy, expert_out, w, inv_perm, dexpert, dw), stream,
@@ -563,8 +565,11 @@ def mr_gather_rows_backward(dxs, k, inv_perm, add=None, dx=None, stream=None):
     _need(inv_perm, "inv_perm", torch.int32, (T * k,))
     if add is not None:
         _need(add, "add", dxs.dtype, (T, d))
-    dx = _new((T, d), dxs.dtype, dxs.device, stream) if dx is None else \
+    if dx is not None:
         _need(dx, "dx", dxs.dtype, (T, d))
+    else:
+        dx = dxs.new_empty((T, d)) if stream is None else \
+            _new((T, d), dxs.dtype, dxs.device, stream)
     _call("mr_gather_rows_backward", _device_of(dxs, inv_perm, add, dx), stream, _ptr(dxs), dt,
           _ptr(inv_perm), _ptr(add), T, d, k, _ptr(dx))
     return dx
@@ -607,7 +612,7 @@ def mr_router_backward(x, W, logits, idx, dw, perm, offsets, route_scale, flags=
     if dx is not None:
         _need(dx, "dx", x.dtype, (T, d))
     elif want_dx:
-        dx = _new((T, d), x.dtype, x.device, stream)
+        dx = torch.empty_like(x) if stream is None else _new((T, d), x.dtype, x.device, stream)
     if dW is not None:
         _need(dW, "dW", torch.float32, (N_r, d))
     elif want_dW:
