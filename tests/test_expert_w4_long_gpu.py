@@ -7,7 +7,7 @@ import torch
 import gradients as gr
 import token_dispatch_fp32_b200 as mr
 from parity import widen
-from test_backward_gpu import _i32
+from test_backward_gpu import _i32, _rows
 from test_expert_w4_gpu import _bound, _problem
 from test_rows_gpu import _dev, _host
 
@@ -115,3 +115,47 @@ def test_short_segments(T, k, N_r, n_out, d, group, sdt):
     want, mag, magx = gr.expert_w4(widen(x), perm, offsets, q, widen(s), group, k)
     gr.check(widen(_host(out)), want, ((d / 128 + 16) * mag + 440 * magx) * 2.0 ** -23, "bf16",
              "out")
+
+
+def test_a_thousand_long_segments():
+    """34 rows on each of 1000 experts, the last 40 assignments dropped and one
+    entry of perm out of range: rows behind the last segment stay, the bad entry
+    is flagged and only its own row is affected."""
+    N_r, n, k, n_out, d, group = 1000, 34000, 8, 96, 136, 32
+    rng = np.random.default_rng(4)
+    x = _rows(rng, (n // k, d), "bf16")
+    q = rng.integers(0, 256, (N_r, n_out, d // 2)).astype(np.uint8)
+    s = _rows(rng, (N_r, n_out, -(-d // group)), "bf16", 0.1)
+    perm = rng.permutation(n).astype(np.int32)
+    offsets = np.minimum(np.arange(N_r + 1) * 34, n - 40).astype(np.int32)
+    W4 = mr.mr_expert_pack_w4(torch.from_numpy(q).cuda(), _dev(s), group)
+    want, mag, _ = gr.expert_w4(widen(x), perm[:n - 40], offsets, q, widen(s), group, k)
+    bound = (group / 8 + d / (2 * group) + 1) * 2.0 ** -23 * mag
+    for bad in (False, True):
+        p = perm.copy()
+        if bad:
+            p[500] = n
+        out = torch.full((n, n_out), 7.0, dtype=torch.bfloat16, device="cuda")
+        mr.mr_expert_gemv_gather_w4(_dev(x), k, _i32(p), _i32(offsets), W4, N_r, n_out, group,
+                                    out=out)
+        assert mr.mr_get_error() == (mr.MR_ERR_DEVICE if bad else mr.MR_OK)
+        keep = np.arange(n - 40) != (500 if bad else -1)
+        gr.check(widen(_host(out))[:n - 40][keep], want[keep], bound[keep], "bf16", "out")
+        assert (out[n - 40:] == 7.0).all()
+
+
+def test_two_layers_at_once():
+    """Layers of long segments on two streams, each as alone."""
+    probs = [_problem(600, 8, 16, 2048, 1032, 32, "bf16", seed) for seed in (1, 2)]
+    calls = []
+    for x, perm, offsets, _, q, s in probs:
+        W4 = mr.mr_expert_pack_w4(torch.from_numpy(q).cuda(), _dev(s), 32)
+        calls.append((_dev(x), 8, _i32(perm), _i32(offsets), W4, 16, 2048, 32))
+    ref = [mr.mr_expert_gemv_gather_w4(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = [mr.mr_expert_gemv_gather_w4(*c, stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert mr.mr_get_error() == mr.MR_OK
