@@ -20,12 +20,13 @@
 //    of the group's columns, which one more MMA pair with a constant operand
 //    forms for all rows at once.
 // Measured: 62 cycles per 16 x 128 weights (about 140 instructions, half of them
-// on the half-rate integer pipe), 66 % of the HBM rate on a decode batch of 64
-// tokens (422 to 442 us); the same kernel without the arithmetic streams at the full
-// rate (272 us).  Subtracting per weight instead took 557 us; 8-bit MMAs, whose
-// e4m3 codes 0 .. 15 are the nibbles themselves, run as two 16-bit ones with
-// unpacking on this GPU (639 us); a ring shared by the CTA with a producer warp
-// 643 us.
+// on the half-rate integer pipe); a decode batch of 64 tokens takes 405 to 445 us
+// from box to box, 63 to 69 % of the HBM rate: 355 us where no warp waits for
+// weights, 272 us for the stream without the arithmetic; the rest (x through L1,
+// the ends of items) is not measured apart.  Subtracting per weight instead took
+// 557 us; 8-bit MMAs, whose e4m3 codes 0 .. 15 are the nibbles themselves, run as
+// two 16-bit ones with unpacking on this GPU (639 us); a ring shared by the CTA
+// with a producer warp 643 us.
 // Every product is exact in fp32.  A group's sum runs through at most 55 * sum
 // |x| (24 + 31) where |q - 8| alone would reach 8 * sum |x|, in fp32; it is
 // then scaled and added in fp32, and the result rounded to bf16 once.
