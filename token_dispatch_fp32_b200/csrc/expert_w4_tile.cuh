@@ -32,13 +32,14 @@
 // Measured (d = 7168, n_out = 2048): 128 rows x 256 experts 2.16 ms with groups of
 // 32 (2.28 with scaled weights in two planes and one accumulation), 1.71 with
 // groups of 128 (2.28); 150 rows x 8 experts (d = 1408, n_out = 2056, groups of 128,
-// fp32 scales: three planes before) 32.8 us (36.9); 192 rows x 8 experts, two blocks
-// each here, 152 us (109 with blocks of 192 rows, whose sums do not fit the
-// registers).  With groups of 32 a stage of 128 columns takes about 2200 cycles, of
-// which reading the four sums from TMEM 1730; with groups of 128 about 1600, bound
-// by the two warps that copy x (1180 to issue, 250 for the copies to land); its
-// MMAs take 600.  Sixteen warps for the sums were 1 to 7 % slower, loads of 32
-// columns 10 %.
+// fp32 scales: three planes before) 32.8 us (36.9); segments of 129 to 192
+// rows are two blocks here and were one, 160 rows x 64 experts 933 us (616), since
+// the sums of 192 rows do not fit the registers.  With groups of 32 a stage of 128
+// columns of 128 rows takes about 2250 cycles, bound by the sums' way out of TMEM: 256
+// KB, two warps a lane quarter at 128 bytes a cycle in all; more warps for them
+// were 1 to 7 % slower, loads of 32 columns 10 %, loads under the additions of the
+// one before 5 %.  With groups of 128 it takes about 1600, bound by the two warps
+// that copy x (1180 to issue, 250 for the copies to land); its MMAs take 600.
 #pragma once
 
 #include "expert_w4.cuh"
